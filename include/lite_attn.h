@@ -370,6 +370,123 @@ int lite_lse_merge(const void* const* outs, const float* const* lses, int n_part
 int lite_dropped_mass(const float* lse_live, const float* lse_full, float* row_mass, float* stats,
                       int B, int H, int N, lite_stream_t stream);
 
+/*
+ * lite_qk_rope -- RMS norm of queries and keys (optional) and rotary positions on several axes, in
+ * one pass: what a video transformer does to q and k between its projection and its attention. No
+ * counterpart on the pages, whose calls take rotated q and k.
+ *
+ * For token n of batch entry b and every head, with d elements x and d/2 pairs:
+ *   norm   x <- x * rsqrt(mean(x^2) + eps) * weight, the mean over the head's d elements
+ *          (norm = 1, weight [d]) or over all the token's heads (norm = 2, weight [heads * d]).
+ *   rotate pair p by phi = pos(axis[p], n) * freq[p]:
+ *          (x0, x1) <- (x0 cos phi - x1 sin phi, x0 sin phi + x1 cos phi).
+ * Angles are formed and reduced in 64 bits, everything else in 32; the output is rounded once.
+ *
+ *  q, k           in   device [B, N, H, d] and [B, N, Hk, d] of type `dtype`; k may be NULL (queries
+ *                      only; Hk, k_out and k's other fields are not looked at then).
+ *  q_out, k_out   out  device bf16, same shapes. Either may be its input itself (same type and
+ *                      strides); other overlaps are not allowed.
+ *  *_stride            strides in elements of the batch, token and head dimension (the head dim is
+ *                      contiguous): non-negative, multiples of 16 bytes. Strides of dimensions with one
+ *                      entry are not looked at. An output's rows may not overlap.
+ *  q_weight, k_weight  device fp32, 16-byte aligned; NULL without norm.
+ *  pairing        0: pair p = elements (2p, 2p + 1); 1: (p, p + d/2).
+ *  freq, axis     HOST [d/2]: angular frequency and axis of each pair (freq 0 leaves a pair as it is).
+ *  n_axes         1 .. 4.
+ *  pos            device positions: fp32 or int32 (pos_dtype), position of (b, axis, n) at
+ *                 b * pos_batch_stride + axis * pos_axis_stride + n (a batch stride of 0 shares them).
+ *                 NULL: token n is cell start + n of the row-major grid grid[0] x .. x
+ *                 grid[n_axes - 1] (HOST), its positions are the cell's coordinates; start + N may not
+ *                 exceed the number of cells.
+ *  The host arrays are read during the call only. d in {64, 128}; (H + Hk) * d <= 32768;
+ *  B * N < 2^31 - 1024. No scratch.
+ */
+enum { LITE_BF16 = 0, LITE_FP16 = 1, LITE_FP32 = 2, LITE_INT32 = 3 };
+typedef struct lite_rope_args {
+  const void* q;
+  const void* k;
+  void* q_out;
+  void* k_out;
+  int64_t q_stride[3], k_stride[3], q_out_stride[3], k_out_stride[3];
+  const float* q_weight;
+  const float* k_weight;
+  const double* freq;
+  const int32_t* axis;
+  const void* pos;
+  int64_t pos_batch_stride, pos_axis_stride;
+  const int64_t* grid;
+  int64_t start;
+  int32_t dtype, pos_dtype, norm, pairing, n_axes;
+  int32_t B, N, H, Hk, d;
+  float eps;
+} lite_rope_args;
+int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream);
+
+/*
+ * lite_attn_span -- attention in which every query row sees one interval of keys.
+ *
+ * lite_attn_dense_ex and the Skip-Mask calls know key tiles only. Here row n of batch entry b sees the
+ * keys m with spans[b][n][0] <= m < spans[b][n][1] (clipped to [0, Nk)): documents packed into one
+ * sequence, a prefix that all rows see, frame-causal and windowed rows, padded batches. A row whose
+ * span is empty gets o = 0 and lse = -inf. Over the keys a row sees:
+ *   s = scale q.k;  s <- cap tanh(s / cap) when cap > 0;
+ *   s <- s - slopes[h] |q_pos[n] - k_pos[m]| when slopes is given;  o = softmax(s) v,
+ *   lse = ln sum exp(s).
+ * Query head h uses key head h / (H / Hk). Key tiles that no row of a query tile sees are not loaded;
+ * keys outside a row's span do not reach its result, whatever k holds there, and v must be finite
+ * in keys that share a 64- or 128-key tile with keys of the row's span.
+ *
+ *  q          in   device bf16 [B, Nq, H, d]; k, v in device bf16 [B, Nk, Hk, d]; strides in elements
+ *                  (batch, token, head; the head dim is contiguous), positive multiples of 8. A batch
+ *                  stride of 0 is one tensor for all entries. Strides of dimensions with one entry
+ *                  are not looked at. 16-byte aligned.
+ *  o          out  device bf16 [B, Nq, H, d], contiguous. lse out device fp32 [B, H, Nq], or NULL.
+ *  spans      in   device int32 [span_batches, Nq, 2], 8-byte aligned, or NULL: all keys.
+ *                  span_batches 1 (one table for all entries) or B.
+ *  scale           <= 0 or NaN selects 1/sqrt(d). cap: 0 = none; negative, infinite or NaN is refused.
+ *  slopes     in   device fp32 [H], or NULL. With slopes:
+ *  q_pos, k_pos    device fp32 [pos_batches, Nq] and [pos_batches, Nk], or NULL each: the queries are
+ *                  the last Nq of all positions (Np + Nk - Nq + n), key m is at Np + m, prefix
+ *                  key m at m (prefix_pos, fp32 [Np], replaces it). pos_batches 1 or B.
+ *  d in {64, 128}; Hk divides H, H / Hk <= 128; B * Nq, Nk, Np, B * H <= 2^30, with slopes Nk + Np and
+ *  Nq <= 2^24. Nk = 0 is refused here (lite_attn_prefix allows it).
+ *
+ * Calls with few query tiles split the keys over the SMs and join the parts with a second kernel; the
+ * parts (and a work counter) come from the library's stream-ordered pool. Results do not depend on
+ * timing: two equal calls give equal bits.
+ */
+typedef struct lite_span_args {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* k_prefix;
+  const void* v_prefix;
+  void* o;
+  float* lse;
+  const int32_t* spans;
+  const float* slopes;
+  const float* q_pos;
+  const float* k_pos;
+  const float* prefix_pos;
+  int64_t q_stride[3], k_stride[3], v_stride[3], k_prefix_stride[3], v_prefix_stride[3];
+  int32_t B, Nq, Nk, Np, H, Hk, d, span_batches, pos_batches;
+  float scale, cap;
+} lite_span_args;
+int lite_attn_span(const lite_span_args* args, lite_stream_t stream);
+
+/*
+ * lite_attn_prefix -- lite_attn_span for a batch whose sequences share a prefix of keys: variants drawn
+ * from one history, guidance branches over the same conditioning frames. Row (b, n) sees all Np prefix
+ * keys and the keys of its span among entry b's own Nk. The prefix is stored once,
+ *
+ *  k_prefix, v_prefix  in  device bf16 [Np, Hk, d], strides as above (the batch stride is not looked at),
+ *
+ * and where sequences have few tokens it is read once for the batch: tokens of several entries are
+ * stacked in one query tile. Np = 0 or Nk = 0 (not both) is allowed. Other arguments as in
+ * lite_attn_span, which ignores the prefix fields.
+ */
+int lite_attn_prefix(const lite_span_args* args, lite_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -10,8 +10,8 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SOURCES = [os.path.join(HERE, "csrc", "lite_attn_api.cu")]
-DEPS = SOURCES + sorted(glob.glob(os.path.join(HERE, "csrc", "*.cuh"))) + [os.path.join(ROOT, "include", "lite_attn.h")]
+SOURCES = [os.path.join(HERE, "csrc", "lite_attn_api.cu"), os.path.join(HERE, "csrc", "span_api.cu")]
+DEPS = SOURCES + sorted(glob.glob(os.path.join(HERE, "csrc", "*.cuh")) + glob.glob(os.path.join(HERE, "csrc", "*.h"))) + [os.path.join(ROOT, "include", "lite_attn.h")]
 OUT = os.path.join(HERE, "liblite_attn.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -33,7 +33,7 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and up_to_date():
         return OUT
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC,-O2",
+    cmd = [nvcc(), *ARCH, "-t0", "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC,-O2",
            "-I", os.path.join(ROOT, "include"), "-o", OUT + ".tmp", *SOURCES, *extra]
     if verbose:
         cmd.insert(-len(SOURCES) - len(extra), "-Xptxas=-v")

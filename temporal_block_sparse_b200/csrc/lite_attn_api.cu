@@ -16,6 +16,7 @@
 
 #include "attn_kernel.cuh"
 #include "calib_kernels.cuh"
+#include "host_common.h"
 #include "lite_attn.h"
 #include "mask_kernels.cuh"
 #include "merge_kernel.cuh"
@@ -107,6 +108,17 @@ int ensure_pool(DeviceCache* c) {
   c->pool = pool;
   return LITE_OK;
 }
+
+}  // namespace
+
+int lite_host::device_context(bool with_pool, DeviceContext* out) {
+  DeviceCache* c = nullptr;
+  if (device_cache(&c) != LITE_OK || (with_pool && ensure_pool(c) != LITE_OK)) return LITE_ERR_CUDA;
+  *out = DeviceContext{c->sms, c->status, c->pool, g_encode, g_opt.wait_limit_ns, g_opt.debug_stall, g_opt.max_ctas};
+  return LITE_OK;
+}
+
+namespace {
 
 bool debug_env() {
   const char* e = std::getenv("LITE_ATTN_DEBUG");

@@ -1,0 +1,778 @@
+// span_kernel.cuh -- attention in which every query row sees one interval ("span") of keys, for
+// sm_100a (tcgen05 + TMEM + TMA): documents packed into one sequence, prefixes, frame-causal and
+// windowed rows, padded batches; optionally with scores capped by a tanh, a bias that grows with
+// distance, grouped key heads, and a prefix of keys that the whole batch shares.
+//
+// For query row n of batch entry b and head h, over the Np shared prefix keys and over the keys
+// m in [start(n), end(n)) of entry b:
+//   s = scale q.k;  s <- cap tanh(s / cap);  s <- s - slope_h |position(n) - position(m)|
+//   o = softmax(s) v,  lse = ln sum exp(s);  a row that sees no key has o = 0, lse = -inf.
+//
+// Rows of a query tile. The MMA takes 128 query rows against one K tile. With grouped heads (G
+// query heads per key head) a tile stacks TN = 128 / G tokens x G heads, so a key tile is read once
+// for all heads that share it. For a shared prefix and few tokens a sequence, a tile stacks
+// tokens of different batch entries (the prefix pass takes the batch as one row of B * Nq tokens),
+// so the prefix is read once for the batch.
+//
+// Work items. An item is a pair of query tiles (one per softmax warpgroup) and a part of the key
+// tiles they see: [prefix tiles][own tiles lo .. hi), of which split s of S takes its share. With
+// S = 1 and one pass the item writes o and lse; otherwise it writes its unnormalised O, row maximum
+// and row sum (32-bit) to scratch, and lite_span_combine_kernel joins the parts in index order.
+//
+// Warp roles (320 threads), barriers and the S -> P -> PV chain are those of lite_attn_kernel
+// (attn_kernel.cuh): warp 0 finds the key range of the item's rows and feeds K and V by TMA, warp 1
+// issues the MMAs, warps 2-5 and 6-9 run the softmax of one query tile each, P staying in TMEM.
+// A key tile that every row of the query tile sees entirely takes no mask instruction; only tiles
+// that a span ends in (and the last one) pay for the comparison.
+//
+// Every wait is bounded as in lite_attn_kernel; on expiry the status word is set and the CTA drains.
+#pragma once
+
+#include "attn_kernel.cuh"
+
+namespace lite {
+
+// 1 / x within one unit in the last place (0 for an infinite x)
+__device__ __forceinline__ float fast_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+constexpr int kSpanCap = 1, kSpanBias = 2;  // MOD bits of the kernel
+
+struct SpanParams {
+  __nv_bfloat16* o;         // [B, Nq, H, D]
+  float* lse;               // [B, H, Nq] or null
+  const int* spans;         // [B or 1, Nq, 2] or null (all keys)
+  long long span_b;         // 2 * Nq, or 0: one table for all batch entries
+  const float* slopes;      // [H] (bias)
+  const float* q_pos;       // [B or 1, Nq] or null: Np + Nk - Nq + n
+  const float* k_pos;       // [B or 1, Nk] or null: Np + m
+  const float* p_pos;       // [Np] or null: m
+  long long q_pos_b, k_pos_b;
+  float* part;              // scratch of the parts, or null: items write o and lse
+  int* work_counter;        // zero before launch; null: static striding over items
+  int* status;
+  unsigned long long wait_limit_ns;
+  int debug_stall;
+  int B, H, Hk, G, Nq, Nk, Np;
+  int q_bm, k_bm, v_bm;     // 0: the tensor is the same for every batch entry, else 1
+  int TN;                   // tokens of a query tile: 128 / G
+  int Tp;                   // prefix key tiles
+  int fused;                // own items walk the prefix tiles too
+  int pre_pairs, pre_splits;  // prefix pass: tile pairs per key head (0: none), parts
+  int own_pairs, own_splits;  // own pass: tile pairs per (b, key head) (0: none), parts
+  int pre_items;            // Hk * pre_pairs * pre_splits
+  int n_items;              // + B * Hk * own_pairs * own_splits
+  float scale_log2;         // softmax scale * log2(e)
+  float cap_a, cap_c;       // 2 scale log2(e) / cap and cap log2(e)
+};
+
+// floats of one part: O rows, then row maxima and row sums of a 128-row tile
+template <int D>
+struct SpanPart {
+  static constexpr size_t FLOATS = 128 * D + 256;
+};
+
+// One query tile of an item: its live key tiles are n_pre prefix tiles from v_first on, then
+// n_live - n_pre own tiles from j_first on.
+struct SpanTile {
+  int tok0;              // its first token (index in the pass: n, or b * Nq + n in the prefix pass)
+  int rows;              // valid rows (0: the tile does not exist)
+  int n_live, n_pre;
+  int j_first;
+  int full_lo, full_hi;  // every row sees the own keys [full_lo, full_hi)
+};
+
+struct SpanInfo {
+  int kind;              // -1 end of the work, 0 own pass, 1 prefix pass
+  int b, hk;
+  int item;              // index of its parts in scratch
+  int v_first;
+  SpanTile t[2];
+};
+
+struct alignas(8) SpanCtl {
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[2], kv_free[2];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t item_full[2], item_empty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  uint32_t ring[4];
+  SpanInfo info[2];
+};
+
+// The span of a token, clipped to [0, Nk).
+__device__ __forceinline__ void span_of(const SpanParams& p, int b, int n, int& s, int& e) {
+  s = 0;
+  e = p.Nk;
+  if (p.spans) {
+    const int2 x = __ldg(reinterpret_cast<const int2*>(p.spans + b * p.span_b + 2ll * n));
+    s = max(x.x, 0);
+    e = min(x.y, p.Nk);
+  }
+  if (e <= s) s = e = 0;
+}
+
+// Decodes item `idx` (whole warp; the result is in every lane).
+template <int BN>
+__device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int lane, SpanInfo& it) {
+  int pair, split, splits, ntok;
+  it.item = idx;
+  if (idx < p.pre_items) {
+    it.kind = 1;
+    splits = p.pre_splits;
+    const int per = p.pre_pairs * splits;
+    it.hk = idx / per;
+    const int rem = idx - it.hk * per;
+    pair = rem / splits;
+    split = rem - pair * splits;
+    it.b = 0;
+    ntok = p.B * p.Nq;
+  } else {
+    it.kind = 0;
+    splits = p.own_splits;
+    const int i = idx - p.pre_items;
+    const int per = p.own_pairs * splits;
+    const int bh = i / per;
+    const int rem = i - bh * per;
+    // the last rows first: where rows see their past, these have the most keys
+    pair = p.own_pairs - 1 - rem / splits;
+    split = rem % splits;
+    it.b = bh / p.Hk;
+    it.hk = bh - it.b * p.Hk;
+    ntok = p.Nq;
+  }
+  const int tp = (it.kind == 1 || p.fused) ? p.Tp : 0;
+  int jlo = 0x7fffffff, jhi = 0;  // own key tiles that either query tile has to see
+  int tlo[2], thi[2];             // and each of them
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    SpanTile& t = it.t[g];
+    t.tok0 = (2 * pair + g) * p.TN;
+    const int toks = max(0, min(p.TN, ntok - t.tok0));
+    t.rows = toks * p.G;
+    tlo[g] = thi[g] = 0;
+    t.full_lo = 0;
+    t.full_hi = p.Nk;
+    if (it.kind == 0 && toks > 0) {
+      int lo = 0x7fffffff, hi = 0, flo = 0, fhi = p.Nk;
+      if (p.spans) {
+        for (int x = lane; x < toks; x += 32) {
+          int s, e;
+          span_of(p, it.b, t.tok0 + x, s, e);
+          if (e > s) {
+            lo = min(lo, s);
+            hi = max(hi, e);
+          }
+          flo = max(flo, e > s ? s : 0x7fffffff);
+          fhi = min(fhi, e);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        flo = __reduce_max_sync(0xffffffffu, flo);
+        fhi = __reduce_min_sync(0xffffffffu, fhi);
+      } else {
+        lo = 0;
+        hi = p.Nk;
+      }
+      if (hi > lo) {
+        tlo[g] = lo / BN;
+        thi[g] = (hi + BN - 1) / BN;
+        jlo = min(jlo, tlo[g]);
+        jhi = max(jhi, thi[g]);
+      }
+      t.full_lo = flo;
+      t.full_hi = fhi;
+    }
+  }
+  if (jhi == 0) jlo = 0;
+  // virtual tiles: prefix [0, tp), then own jlo .. jhi; this split's are [v0, v1)
+  const long long total = tp + (jhi - jlo);
+  const int v0 = int(total * split / splits), v1 = int(total * (split + 1) / splits);
+  it.v_first = v0;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    SpanTile& t = it.t[g];
+    t.n_pre = t.rows ? max(0, min(v1, tp) - v0) : 0;
+    const int j0 = max(tlo[g], jlo + max(v0 - tp, 0)), j1 = min(thi[g], jlo + v1 - tp);
+    t.j_first = j0;
+    t.n_live = t.n_pre + (t.rows ? max(0, j1 - j0) : 0);
+  }
+}
+
+// Shared memory: lite_attn_kernel's layout, with a staging area of 32 rows x 128 bytes a softmax warp.
+template <int D, int BN>
+struct SpanCfg : AttnCfg<D, BN> {
+  using A = AttnCfg<D, BN>;
+  static constexpr int OST_WARP = 32 * 128;
+  static constexpr int SMEM_USED = A::OFF_OST + 8 * OST_WARP + 1024;
+  static constexpr int SMEM_BYTES =
+      A::CTAS_PER_SM == 2 ? SMEM_USED : (SMEM_USED > 120 * 1024 ? SMEM_USED : 120 * 1024);
+  static_assert(A::CTAS_PER_SM == 1 || 2 * (SMEM_BYTES + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+template <int D, int BN, int MOD>
+__global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
+    lite_span_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQp,
+                     const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                     const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
+                     const SpanParams p) {
+  using C = SpanCfg<D, BN>;
+  constexpr bool CAP = (MOD & kSpanCap) != 0, BIAS = (MOD & kSpanBias) != 0;
+  static_assert(sizeof(SpanCtl) <= C::CTL_BYTES, "control block");
+  // key positions of two tiles per warpgroup share the group's staging area
+  static_assert(2 * BN * 4 <= 4 * C::OST_WARP, "position buffer");
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  SpanCtl* ctl = reinterpret_cast<SpanCtl*>(smem + C::OFF_CTL);
+  const uint32_t sQ = ptx::smem_addr(smem + C::OFF_Q);
+  const uint32_t sK = ptx::smem_addr(smem + C::OFF_K);
+  const uint32_t sV = ptx::smem_addr(smem + C::OFF_V);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+#define BAR(x) ptx::smem_addr(&ctl->x)
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(BAR(q_full), 1);
+    ptx::mbar_init(BAR(q_empty), 1);
+    for (int b = 0; b < 2; ++b) {
+      ptx::mbar_init(BAR(kv_full[b]), 1);
+      ptx::mbar_init(BAR(kv_free[b]), 1);
+      ptx::mbar_init(BAR(s_full[b]), 1);
+      ptx::mbar_init(BAR(p_full[b]), 128);
+      ptx::mbar_init(BAR(pv_done[b]), 1);
+      ptx::mbar_init(BAR(o_free[b]), 128);
+      ptx::mbar_init(BAR(item_full[b]), 1);
+      ptx::mbar_init(BAR(item_empty[b]), 8);
+    }
+    ptx::mbar_init(BAR(drain), 1);
+    ctl->abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_addr(&ctl->tmem_base), C::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = ctl->tmem_base;
+  const Waiter wt{&ctl->abort, p.status, p.wait_limit_ns};
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------------- TMA producer
+    // Bundles as in lite_attn_kernel: bundle u carries K_u and V_{u-1}; kv_free of u-2 frees both
+    // stages. The whole warp decodes an item (it reads the spans of the item's tokens), lane 0
+    // issues the loads.
+    uint32_t u = 0, items = 0, qn = 0;
+    bool ok = true;
+    bool q_armed = false, kv_armed[2] = {false, false};
+    uint32_t q_par = 0, kv_par[2] = {0, 0};
+    bool v_needed = false, pv_pre = false;
+    int pj = 0, ph = 0, pb = 0;  // V coordinates of union tile u-1
+    auto bundle = [&](bool with_k, bool pre, int j, int h, int b, uint32_t flags) -> bool {
+      if (u >= 2 && !wt.wait(BAR(kv_free[u & 1]), ((u - 2) >> 1) & 1)) return false;
+      ctl->ring[u & 3] = flags;
+      const uint32_t bar = BAR(kv_full[u & 1]);
+      ptx::mbar_arrive_expect_tx(bar, (with_k ? C::KV_TX : 0u) + (v_needed ? C::KV_TX : 0u));
+      if (with_k)
+        ptx::tma_load_5d(sK + (u & 1) * C::KV_BYTES, pre ? &tmKp : &tmK, bar, 0, j * BN, 0, h, pre ? 0 : b * p.k_bm);
+      if (v_needed)
+        ptx::tma_load_5d(sV + ((u - 1) & 1) * C::KV_BYTES, pv_pre ? &tmVp : &tmV, bar, 0, pj * BN, 0, ph,
+                         pv_pre ? 0 : pb * p.v_bm);
+      v_needed = with_k;
+      kv_armed[u & 1] = true;
+      kv_par[u & 1] = (u >> 1) & 1;
+      pv_pre = pre;
+      pj = j;
+      ph = h;
+      pb = b;
+      ++u;
+      return true;
+    };
+    const uint32_t q_rows = uint32_t(p.TN * p.G);
+    while (true) {
+      const int slot = items & 1;
+      int item = -1;
+      if (lane == 0) {
+        if (items >= 2) ok = wt.wait(BAR(item_empty[slot]), ((items >> 1) - 1) & 1);
+        if (ok) item = p.work_counter ? atomicAdd(p.work_counter, 1) : int(blockIdx.x + items * gridDim.x);
+        if (item >= p.n_items) item = -1;
+      }
+      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+      if (!ok) break;
+      item = __shfl_sync(0xffffffffu, item, 0);
+      SpanInfo it;
+      it.kind = -1;
+      if (item >= 0) span_decode<BN>(p, item, lane, it);
+      if (lane == 0) {
+        ctl->info[slot] = it;
+        ptx::mbar_arrive(BAR(item_full[slot]));
+      }
+      ++items;
+      if (item < 0) break;
+      if (lane == 0) {
+        const int n0 = it.t[0].n_live, n1 = it.t[1].n_live;
+        if (n0 + n1 == 0) {
+          // flush the pending V of the item before, as lite_attn_kernel does for an empty item
+          if (v_needed) ok = bundle(false, false, 0, 0, 0, 0u);
+        } else {
+          if (qn >= 1) ok = wt.wait(BAR(q_empty), (qn - 1) & 1);
+          if (ok) {
+            const uint32_t qtx = q_rows * 128u * C::NCHUNK;
+            ptx::mbar_arrive_expect_tx(BAR(q_full), (n0 > 0 ? qtx : 0u) + (n1 > 0 ? qtx : 0u));
+            for (int g = 0; g < 2; ++g)
+              if ((g ? n1 : n0) > 0)
+                for (int c = 0; c < C::NCHUNK; ++c)
+                  ptx::tma_load_5d(sQ + g * C::Q_BYTES + c * C::Q_CHUNK, it.kind == 1 ? &tmQp : &tmQ, BAR(q_full),
+                                   c * 64, 0, it.t[g].tok0, it.hk, it.kind == 1 ? 0 : it.b * p.q_bm);
+            q_armed = true;
+            q_par = qn & 1;
+            const uint32_t item_bits = ((qn & 1) ? kItemOdd : 0u) | (qn >= 1 ? kItemAfterFirst : 0u);
+            uint32_t f = kItemFirst;
+            // the union of the two tiles' key tiles: prefix tiles (common to both), then own ones in order
+            int d0 = 0, d1 = 0;
+            while (ok && (d0 < n0 || d1 < n1)) {
+              const bool pre0 = d0 < it.t[0].n_pre, pre1 = d1 < it.t[1].n_pre;
+              const int none = 0x7fffffff;
+              int c0 = none, c1 = none, j;
+              bool pre = pre0 || pre1;
+              if (pre) {
+                if (pre0) c0 = it.v_first + d0;
+                if (pre1) c1 = it.v_first + d1;
+              } else {
+                if (d0 < n0) c0 = it.t[0].j_first + d0 - it.t[0].n_pre;
+                if (d1 < n1) c1 = it.t[1].j_first + d1 - it.t[1].n_pre;
+              }
+              j = min(c0, c1);
+              f |= item_bits;
+              if (c0 == j) {
+                f |= kLive0 | (d0 == 0 ? kFirst0 : 0u) | (d0 == n0 - 1 ? kLast0 : 0u);
+                ++d0;
+              }
+              if (c1 == j) {
+                f |= kLive1 | (d1 == 0 ? kFirst1 : 0u) | (d1 == n1 - 1 ? kLast1 : 0u);
+                ++d1;
+              }
+              if (d0 == n0 && d1 == n1) f |= kItemLast;
+              ok = bundle(true, pre, j, it.hk, it.b, f);
+              f = 0u;
+            }
+            ++qn;
+          }
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, int(ok), 0) != 0;
+      if (!ok) break;
+    }
+    if (lane == 0) {
+      if (ok) bundle(false, false, 0, 0, 0, kEnd);
+      if (q_armed) wt.wait_drain(BAR(q_full), q_par);
+      for (int b = 0; b < 2; ++b)
+        if (kv_armed[b]) wt.wait_drain(BAR(kv_full[b]), kv_par[b]);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------------- MMA issuer
+    // The protocol of lite_attn_kernel: per union tile PV_g(u-1), then QK_g(u), for g = 0, 1.
+    if (lane == 0) {
+      uint32_t u = 0;
+      uint32_t pc[2] = {0, 0};
+      uint32_t prev = 0;
+      bool ok = true;
+      const uint64_t q_desc0 = umma_desc_sw128(sQ, 16, 1024);
+      const uint64_t k_desc0 = umma_desc_sw128(sK, 16, 1024);
+      const uint64_t v_desc0 = umma_desc_sw128(sV, C::KV_CHUNK, 1024);
+      const uint32_t bar_kv = BAR(kv_full[0]), bar_free = BAR(kv_free[0]);
+      if (p.debug_stall) {
+        const uint64_t s0 = ptx::globaltimer();
+        while (!ctl->abort && ptx::globaltimer() - s0 < 4ull * p.wait_limit_ns) {
+        }
+        if (!ctl->abort) wt.give_up();
+        ok = false;
+      }
+      while (ok) {
+        if (!wt.wait(bar_kv + (u & 1) * 8, (u >> 1) & 1)) break;
+        const uint32_t f = ctl->ring[u & 3];
+        ptx::tc_fence_after();
+        bool need_q = (f & kItemFirst) != 0u;
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          if (prev & (kLive0 << g)) {
+            if ((prev & (kFirst0 << g)) && (prev & kItemAfterFirst) &&
+                !wt.wait(BAR(o_free[g]), (prev & kItemOdd) ? 0u : 1u)) {
+              ok = false;
+              break;
+            }
+            if (!wt.wait(BAR(p_full[g]), pc[g] & 1)) {
+              ok = false;
+              break;
+            }
+            ++pc[g];
+            ptx::tc_fence_after();
+            const uint32_t p_tmem = tmem + C::S_COL + g * BN;
+            const uint32_t o_tmem = tmem + C::O_COL + g * D;
+            const uint64_t vd = v_desc0 + uint64_t((((u - 1) & 1) * C::KV_BYTES) >> 4);
+            const bool fresh = (prev & (kFirst0 << g)) != 0u;
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              ptx::mma_ts(o_tmem, p_tmem + kk * 8, vd + uint64_t(kk * 128), C::IDESC_PV, (fresh && kk == 0) ? 0u : 1u);
+            if (prev & (kLast0 << g)) ptx::mma_commit(BAR(pv_done[g]));
+          }
+          if (f & (kLive0 << g)) {
+            if (need_q) {
+              if (!wt.wait(BAR(q_full), (f & kItemOdd) ? 1u : 0u)) {
+                ok = false;
+                break;
+              }
+              ptx::tc_fence_after();
+              need_q = false;
+            }
+            const uint64_t qd = q_desc0 + uint64_t((g * C::Q_BYTES) >> 4);
+            const uint64_t kd = k_desc0 + uint64_t(((u & 1) * C::KV_BYTES) >> 4);
+            const uint32_t s_tmem = tmem + C::S_COL + g * BN;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = uint64_t((kk >> 2) * (C::Q_CHUNK >> 4) + (kk & 3) * 2);
+              const uint64_t offk = uint64_t((kk >> 2) * (C::KV_CHUNK >> 4) + (kk & 3) * 2);
+              ptx::mma_ss(s_tmem, qd + off, kd + offk, C::IDESC_QK, kk > 0 ? 1u : 0u);
+            }
+            ptx::mma_commit(BAR(s_full[g]));
+          }
+        }
+        if (!ok || (f & kEnd)) break;
+        ptx::mma_commit(bar_free + (u & 1) * 8);
+        if (f & kItemLast) ptx::mma_commit(BAR(q_empty));
+        prev = f;
+        ++u;
+      }
+      ptx::mma_commit(BAR(drain));
+      wt.wait_drain(BAR(drain), 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------------- softmax warpgroups
+    const int grp = (warp - 2) >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;  // TMEM lane = row of the query tile
+    const uint32_t lane_base = uint32_t(quarter * 32) << 16;
+    const uint32_t gbar = 1 + grp;
+    uint8_t* stage = smem + C::OFF_OST + (grp * 4 + quarter) * C::OST_WARP;
+    float* kpos = reinterpret_cast<float*>(smem + C::OFF_OST + grp * 4 * C::OST_WARP);  // two tiles (bias)
+    const uint32_t s_tmem = tmem + lane_base + C::S_COL + grp * BN;
+    const uint32_t o_tmem = tmem + lane_base + C::O_COL + grp * D;
+    const int r_tok = r / p.G, r_head = r - r_tok * p.G;
+    // batch entry, token and head of this thread's row in the item
+    auto row_of = [&](const SpanInfo* it, int& b, int& n, int& h) {
+      b = it->b;
+      n = it->t[grp].tok0 + r_tok;
+      if (it->kind == 1) {
+        b = n / p.Nq;
+        n -= b * p.Nq;
+      }
+      h = it->hk * p.G + r_head;
+    };
+    uint32_t tg = 0, items = 0, pv_phase = 0;
+    while (true) {
+      const int slot = items & 1;
+      bool ok = wt.wait(BAR(item_full[slot]), (items >> 1) & 1);
+      const SpanInfo* it = &ctl->info[slot];  // released (item_empty) at the end of the item
+      const SpanTile* mt = &it->t[grp];
+      ++items;
+      if (!ptx::named_bar_and(gbar, 128, ok) || it->kind < 0) break;
+      const int n_live = mt->n_live;
+      const bool valid = r < mt->rows;
+      const bool warp_valid = quarter * 32 < mt->rows;  // the warp has a valid row
+      int ks = 0, ke = 0;
+      float slope = 0.f, qp = 0.f;
+      if (valid) {
+        int b, n, h;
+        row_of(it, b, n, h);
+        if (it->kind == 0) span_of(p, b, n, ks, ke);
+        if (BIAS) {
+          slope = __ldg(p.slopes + h) * 1.4426950408889634f;
+          qp = p.q_pos ? __ldg(p.q_pos + b * p.q_pos_b + n) : float(p.Np + p.Nk - p.Nq + n);
+        }
+      }
+      float m_used = -INFINITY;  // exponent reference (lazy rescale), log2 units
+      float l = 0.f;             // row sum relative to m_used
+      for (int idx = 0; idx < n_live; ++idx) {
+        const bool pre = idx < mt->n_pre;
+        const int j0 = (pre ? it->v_first + idx : mt->j_first + idx - mt->n_pre) * BN;  // the tile's first key
+        float* kp = kpos + (idx & 1) * BN;
+        if (BIAS) {
+          // thread r brings the position of key r; the buffer's last readers passed the barrier of
+          // the tile before
+          if (r < BN) {
+            const int m = j0 + r;
+            float x = 0.f;
+            if (pre) {
+              if (m < p.Np) x = p.p_pos ? __ldg(p.p_pos + m) : float(m);
+            } else {
+              if (m < p.Nk) x = p.k_pos ? __ldg(p.k_pos + it->b * p.k_pos_b + m) : float(p.Np + m);
+            }
+            kp[r] = x;
+          }
+          ptx::named_bar_sync(gbar, 128);
+        }
+        wt.wait(BAR(s_full[grp]), tg & 1);
+        ++tg;
+        __syncwarp();
+        ptx::tc_fence_after();
+        if (warp_valid) {
+          uint32_t sr[BN];
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c)
+            ptx::tmem_ld32(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          ptx::tmem_wait_ld();
+          float s[BN];
+#pragma unroll
+          for (int x = 0; x < BN; ++x) s[x] = __uint_as_float(sr[x]);
+          if (CAP) {
+            // cap tanh(z) = cap - 2 cap / (1 + e^{2z}), in log2 units; both ends saturate exactly
+#pragma unroll
+            for (int x = 0; x < BN; ++x)
+              s[x] = fmaf(-2.f * p.cap_c, fast_rcp(1.f + ptx::ex2(s[x] * p.cap_a)), p.cap_c);
+          }
+          if (BIAS) {
+#pragma unroll
+            for (int x = 0; x < BN; x += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(kp + x);
+              const float dd[4] = {k4.x - qp, k4.y - qp, k4.z - qp, k4.w - qp};
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float base = CAP ? s[x + y] : s[x + y] * p.scale_log2;
+                s[x + y] = fmaf(-slope, fabsf(dd[y]), base);
+              }
+            }
+          }
+          // columns [lo, hi) of the tile are keys that this row sees
+          const int lo = pre ? 0 : ks - j0, hi = pre ? p.Np - j0 : ke - j0;
+          const bool masked = pre ? hi < BN : (mt->full_lo > j0 || mt->full_hi < j0 + BN);
+          if (masked) {
+            // each half-word of 32 columns as a bit mask, then one select per column
+#pragma unroll
+            for (int c = 0; c < BN / 32; ++c) {
+              const int a = min(max(lo - 32 * c, 0), 32), z = min(max(hi - 32 * c, 0), 32);
+              const uint32_t upto = z >= 32 ? 0xffffffffu : ((1u << z) - 1u);
+              const uint32_t below = a >= 32 ? 0xffffffffu : ((1u << a) - 1u);
+              const uint32_t bits = upto & ~below;
+#pragma unroll
+              for (int x = 0; x < 32; ++x)
+                s[32 * c + x] = (bits & (1u << x)) ? s[32 * c + x] : -INFINITY;
+            }
+          }
+          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < BN; x += 8) {
+            m0 = ptx::fmax3(m0, s[x], s[x + 1]);
+            m1 = ptx::fmax3(m1, s[x + 2], s[x + 3]);
+            m2 = ptx::fmax3(m2, s[x + 4], s[x + 5]);
+            m3 = ptx::fmax3(m3, s[x + 6], s[x + 7]);
+          }
+          const float to_log2 = MOD ? 1.f : p.scale_log2;
+          const float loc = ptx::fmax3(m0, m1, fmaxf(m2, m3)) * to_log2;
+          const bool need = loc > m_used + kRescaleLog2;
+          float alpha = 1.f;
+          if (need) {
+            alpha = ptx::ex2(m_used - loc);
+            m_used = loc;
+            l *= alpha;
+          }
+          // a row that has seen no key yet keeps m_used = -inf; its exponents are -inf - 0
+          const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+          const float2 sc2 = make_float2(to_log2, to_log2);
+          const float2 nm2 = make_float2(neg_m, neg_m);
+          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < BN / 32; ++c) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int x = 0; x < 16; ++x) {
+              const float2 sx = make_float2(s[32 * c + 2 * x], s[32 * c + 2 * x + 1]);
+              const float2 a = MOD ? __fadd2_rn(sx, nm2) : __ffma2_rn(sx, sc2, nm2);
+              const float2 pp = make_float2(ptx::ex2(a.x), ptx::ex2(a.y));
+              acc[x & 3] = __fadd2_rn(acc[x & 3], pp);
+              __nv_bfloat162 h2 = __floats2bfloat162_rn(pp.x, pp.y);
+              pk[x] = *reinterpret_cast<uint32_t*>(&h2);
+            }
+            ptx::tmem_st16(s_tmem + c * 16, pk);
+          }
+          if (__any_sync(0xffffffffu, need) && idx >= 1) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t rr[32];
+              ptx::tmem_ld32(o_tmem + c * 32, rr);
+              ptx::tmem_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 32; ++x) rr[x] = __float_as_uint(__uint_as_float(rr[x]) * alpha);
+              ptx::tmem_st32(o_tmem + c * 32, rr);
+            }
+          }
+          ptx::tmem_wait_st();
+          const float2 acc2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+          l += acc2.x + acc2.y;
+        }
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(BAR(p_full[grp]));
+      }
+      // ----- epilogue
+      if (BIAS) ptx::named_bar_sync(gbar, 128);  // the position buffer becomes the staging area
+      if (n_live > 0) {
+        wt.wait(BAR(pv_done[grp]), pv_phase & 1);
+        ++pv_phase;
+        __syncwarp();
+        ptx::tc_fence_after();
+      }
+      // a row that saw no key: o = 0, lse = -inf (l is 0 then; a NaN score leaves its mark in l)
+      const bool empty = l == 0.f;
+      if (p.part) {
+        float* part = p.part + (size_t(it->item) * 2 + grp) * SpanPart<D>::FLOATS;
+        if (warp_valid) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t rr[32];
+            ptx::tmem_ld32(o_tmem + c * 32, rr);
+            ptx::tmem_wait_ld();
+            float4* dst = reinterpret_cast<float4*>(part + r * D + c * 32);
+            // (a part without keys is not read: its row sum says so)
+            if (valid && !empty)
+#pragma unroll
+              for (int x = 0; x < 8; ++x)
+                dst[x] = make_float4(__uint_as_float(rr[4 * x]), __uint_as_float(rr[4 * x + 1]),
+                                     __uint_as_float(rr[4 * x + 2]), __uint_as_float(rr[4 * x + 3]));
+          }
+          if (valid) {
+            part[128 * D + r] = m_used;
+            part[128 * D + 128 + r] = l;
+          }
+        }
+        ptx::tc_fence_before();
+        if (it->t[0].n_live + it->t[1].n_live > 0) ptx::mbar_arrive(BAR(o_free[grp]));
+      } else {
+        // Rows go out through the warp's staging area, 64 columns of its 32 rows at a time, so that
+        // its lanes write 128-byte pieces (a tile's rows may belong to several tokens, heads and batch
+        // entries, so there is no box to store).
+        const float inv_l = empty ? 0.f : 1.f / l;
+        int b, n, h;
+        row_of(it, b, n, h);
+        const long long o_row = (static_cast<long long>(b) * p.Nq + n) * p.H + h;
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          if (!warp_valid) break;
+          __syncwarp();
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t rr[32];
+            ptx::tmem_ld32(o_tmem + c * 64 + half * 32, rr);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              uint32_t w[4];
+#pragma unroll
+              for (int y = 0; y < 4; ++y) {
+                const float a = __uint_as_float(rr[8 * x + 2 * y]) * inv_l;
+                const float z = __uint_as_float(rr[8 * x + 2 * y + 1]) * inv_l;
+                const __nv_bfloat162 h2 = __floats2bfloat162_rn(a, z);
+                w[y] = empty ? 0u : *reinterpret_cast<const uint32_t*>(&h2);
+              }
+              *reinterpret_cast<uint4*>(stage + lane * 128 + (((half * 4 + x) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int srow = i * 4 + (lane >> 3), x = lane & 7;
+            const long long row = __shfl_sync(0xffffffffu, o_row, srow);
+            if (quarter * 32 + srow < mt->rows)
+              *reinterpret_cast<uint4*>(p.o + row * D + c * 64 + x * 8) =
+                  *reinterpret_cast<const uint4*>(stage + srow * 128 + ((x ^ (srow & 7)) << 4));
+          }
+        }
+        ptx::tc_fence_before();
+        if (it->t[0].n_live + it->t[1].n_live > 0) ptx::mbar_arrive(BAR(o_free[grp]));
+        if (valid && p.lse)
+          p.lse[(size_t(b) * p.H + h) * p.Nq + n] =
+              empty ? -INFINITY : (m_used + __log2f(l)) * 0.6931471805599453f;
+        if (BIAS) ptx::named_bar_sync(gbar, 128);  // before the next item's positions overwrite the staging
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(BAR(item_empty[slot]));
+    }
+  }
+#undef BAR
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// Joins the parts of every output row: M = max m_i, o = sum 2^(m_i - M) O_i / L, L = sum 2^(m_i - M) l_i.
+// One group of D/4 lanes per row. Bound by the parts' bytes; they were written just before and are in L2.
+template <int D>
+__global__ void __launch_bounds__(256) lite_span_combine_kernel(const SpanParams p) {
+  constexpr int L = D / 4;  // lanes of a row
+  const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / L;
+  const int lane = threadIdx.x % L;
+  if (row >= static_cast<long long>(p.B) * p.Nq * p.H) return;
+  const int h = int(row % p.H);
+  const long long bn = row / p.H;
+  const int b = int(bn / p.Nq), n = int(bn - static_cast<long long>(b) * p.Nq);
+  const int hk = h / p.G, gh = h - hk * p.G;
+  const float* part[2] = {nullptr, nullptr};
+  int count[2] = {0, 0}, at[2] = {0, 0};
+  if (p.pre_pairs) {
+    const int tok = int(bn), tile = tok / p.TN;
+    at[0] = (tok - tile * p.TN) * p.G + gh;
+    part[0] = p.part + (size_t(hk * p.pre_pairs + (tile >> 1)) * p.pre_splits * 2 + (tile & 1)) * SpanPart<D>::FLOATS;
+    count[0] = p.pre_splits;
+  }
+  if (p.own_pairs) {
+    const int tile = n / p.TN;
+    at[1] = (n - tile * p.TN) * p.G + gh;
+    const size_t item = p.pre_items + (size_t(b * p.Hk + hk) * p.own_pairs + (p.own_pairs - 1 - (tile >> 1))) * p.own_splits;
+    part[1] = p.part + (item * 2 + (tile & 1)) * SpanPart<D>::FLOATS;
+    count[1] = p.own_splits;
+  }
+  constexpr size_t STEP = 2 * SpanPart<D>::FLOATS;  // from one split's part to the next's
+  float m = -INFINITY;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < count[k]; ++i) m = fmaxf(m, part[k][i * STEP + 128 * D + at[k]]);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float tot = 0.f;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    for (int i = 0; i < count[k]; ++i) {
+      const float* q = part[k] + i * STEP;
+      const float mi = q[128 * D + at[k]], li = q[128 * D + 128 + at[k]];
+      if (li == 0.f) continue;  // the part saw no key
+      const float w = m == -INFINITY ? 1.f : exp2f(mi - m);
+      const float4 x = *reinterpret_cast<const float4*>(q + at[k] * D + lane * 4);
+      acc.x = fmaf(w, x.x, acc.x);
+      acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z);
+      acc.w = fmaf(w, x.w, acc.w);
+      tot = fmaf(w, li, tot);
+    }
+  const float inv = tot == 0.f ? 0.f : 1.f / tot;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), z = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+  uint2 out;
+  out.x = *reinterpret_cast<const uint32_t*>(&a);
+  out.y = *reinterpret_cast<const uint32_t*>(&z);
+  *reinterpret_cast<uint2*>(p.o + row * D + lane * 4) = out;
+  if (p.lse && lane == 0)
+    p.lse[(size_t(b) * p.H + h) * p.Nq + n] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * 0.6931471805599453f;
+}
+
+}  // namespace lite

@@ -52,6 +52,9 @@ SIGNATURES = {
     "lite_mask_to_ranges": ([_P, _P, _P, _I, _I, _I, _I, _P], _I),
     "lite_set_cta_timing": ([_P, _I], _I),
     "lite_scratch_pool_bytes": ([ctypes.POINTER(ctypes.c_longlong)], _I),
+    "lite_qk_rope": ([_P, _P], _I),
+    "lite_attn_span": ([_P, _P], _I),
+    "lite_attn_prefix": ([_P, _P], _I),
     "lite_attn_fwd_list": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P], _I),
 }
 MAX_MERGE_PARTS = 8
@@ -429,3 +432,312 @@ def lite_set_cta_timing(buf: Optional[torch.Tensor]):
     if buf.dtype != torch.int64 or buf.dim() != 2 or buf.shape[1] != 3 or not buf.is_contiguous():
         raise ValueError("buf must be a contiguous int64 [capacity, 3] tensor")
     _check("lite_set_cta_timing", load().lite_set_cta_timing(buf.data_ptr(), buf.shape[0]))
+
+
+# ---- rotary positions, span attention, shared prefixes
+
+LITE_BF16, LITE_FP16, LITE_FP32, LITE_INT32 = 0, 1, 2, 3
+_I32, _I64 = ctypes.c_int32, ctypes.c_int64
+_S3 = _I64 * 3
+
+
+class _RopeArgs(ctypes.Structure):
+    """lite_rope_args of include/lite_attn.h."""
+
+    _fields_ = [(n, _P) for n in ("q", "k", "q_out", "k_out")]
+    _fields_ += [(n, _S3) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+    _fields_ += [(n, _P) for n in ("q_weight", "k_weight", "freq", "axis", "pos")]
+    _fields_ += [("pos_batch_stride", _I64), ("pos_axis_stride", _I64), ("grid", _P), ("start", _I64)]
+    _fields_ += [(n, _I32) for n in ("dtype", "pos_dtype", "norm", "pairing", "n_axes", "B", "N", "H", "Hk", "d")]
+    _fields_ += [("eps", _F)]
+
+
+class _SpanArgs(ctypes.Structure):
+    """lite_span_args of include/lite_attn.h."""
+
+    _fields_ = [(n, _P) for n in ("q", "k", "v", "k_prefix", "v_prefix", "o", "lse", "spans", "slopes", "q_pos",
+                                  "k_pos", "prefix_pos")]
+    _fields_ += [(n, _S3) for n in ("q_stride", "k_stride", "v_stride", "k_prefix_stride", "v_prefix_stride")]
+    _fields_ += [(n, _I32) for n in ("B", "Nq", "Nk", "Np", "H", "Hk", "d", "span_batches", "pos_batches")]
+    _fields_ += [("scale", _F), ("cap", _F)]
+
+
+def _call_on(fn: str, args, device: torch.device, stream):
+    """Calls library function `fn` on `stream` (default: the current stream of `device`) with `device` current."""
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if device.index == torch.cuda.current_device():
+        st = getattr(load(), fn)(ctypes.addressof(args), stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            st = getattr(load(), fn)(ctypes.addressof(args), stream.cuda_stream)
+    if st != LITE_OK:
+        raise LiteAttnError(fn, st)
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """An output made for work on `stream`: its memory is not handed out again before that work is done."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _check_stream(stream, device):
+    if stream is not None and stream.device != device:
+        raise ValueError("stream must be on the device of q")
+
+
+def _check_rows(name: str, t: torch.Tensor, dtypes, unit: int, device, batch_zero: bool = False):
+    """A CUDA tensor [B, N, heads, d] of one of `dtypes` on `device` whose head dimension is
+    contiguous and whose other strides are multiples of `unit` elements (16 bytes)."""
+    if t.dim() != 4 or not t.is_cuda or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be a 4-D CUDA tensor [B, N, heads, d] of type "
+                         f"{' or '.join(str(x)[6:] for x in dtypes)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the device of q")
+    size, stride = t.shape, t.stride()
+    if size[3] > 1 and stride[3] != 1:
+        raise ValueError(f"{name}: the head dimension must be contiguous")
+    for x in range(3):
+        if size[x] > 1 and (stride[x] % unit or stride[x] < (0 if x == 0 and batch_zero else 1)):
+            raise ValueError(f"{name}: strides must be positive multiples of 16 bytes")
+    if t.data_ptr() % 16:
+        raise ValueError(f"{name} must be 16-byte aligned")
+
+
+def _strides(t: torch.Tensor):
+    st = t.stride()
+    return _S3(st[0], st[1], st[2])
+
+
+class RopePlan:
+    """Frequencies of a rotary embedding over several axes (host data; made once).
+
+    dims: dimensions of the head that each axis turns, e.g. (44, 42, 42) for frame, row and column at
+    d = 128 (workload.axis_split); each even. Pairs beyond their sum are left as they are when
+    `head_dim` is larger. Pair i of an axis with D dims has frequency theta ** (-2 i / D).
+    pairing: "interleaved" turns elements (2p, 2p + 1) together, "half" elements (p, p + d/2).
+    freqs: frequencies of all pairs, in order, to use instead (d/2 numbers; scaled or sectioned variants).
+    """
+
+    def __init__(self, dims, theta: float = 10000.0, pairing: str = "interleaved", head_dim: Optional[int] = None,
+                 freqs=None):
+        dims = tuple(int(x) for x in dims)
+        if not 1 <= len(dims) <= 4 or any(x < 0 or x % 2 for x in dims):
+            raise ValueError("dims: one to four even, non-negative numbers")
+        if pairing not in ("interleaved", "half"):
+            raise ValueError("pairing must be 'interleaved' or 'half'")
+        d = sum(dims) if head_dim is None else int(head_dim)
+        if d not in (64, 128) or sum(dims) > d:
+            raise ValueError("the head dimension must be 64 or 128 and hold the sum of dims")
+        if not (theta > 0.0 and math.isfinite(theta)):
+            raise ValueError("theta must be a positive number")
+        self.dims, self.theta, self.pairing, self.d = dims, float(theta), pairing, d
+        axis = [a for a, x in enumerate(dims) for _ in range(x // 2)]
+        freq = [theta ** (-2.0 * i / x) for x in dims for i in range(x // 2)]
+        spare = d // 2 - len(axis)
+        axis, freq = axis + [0] * spare, freq + [0.0] * spare
+        if freqs is not None:
+            freq = [float(x) for x in freqs]
+            if len(freq) != d // 2 or not all(math.isfinite(x) for x in freq):
+                raise ValueError(f"freqs: {d // 2} finite numbers")
+        self.axis, self.freq = axis, freq
+        self._axis = (_I32 * len(axis))(*axis)
+        self._freq = (ctypes.c_double * len(freq))(*freq)
+
+
+_ROPE_TYPES = {torch.bfloat16: LITE_BF16, torch.float16: LITE_FP16, torch.float32: LITE_FP32}
+
+
+def _check_weight(name: str, w: torch.Tensor, sizes, device):
+    if w.dtype != torch.float32 or not w.is_contiguous() or w.device != device or w.dim() != 1 or w.numel() not in sizes:
+        raise ValueError(f"{name} must be a contiguous fp32 tensor of {' or '.join(str(x) for x in sizes)} elements "
+                         "on the device of q")
+
+
+def lite_qk_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan, grid=None, start: int = 0,
+                 pos: Optional[torch.Tensor] = None, q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, q_out: Optional[torch.Tensor] = None,
+                 k_out: Optional[torch.Tensor] = None, stream=None):
+    """RMS norm (with weights) and rotary positions of q [B, N, H, d] and k [B, N, Hk, d] or None
+    (bf16, fp16 or fp32, any strides that are multiples of 16 bytes, e.g. slices of a fused
+    projection). Returns (q_out, k_out), bf16.
+
+    Positions: token n is cell start + n of the row-major `grid` (one size per axis of the plan), or
+    `pos` [axes, N] or [B, axes, N] (fp32 or int32) gives them. Weights of d elements norm every head by
+    itself, weights of heads * d elements norm the token's whole row. q_out / k_out may be given (a
+    slice of a key cache, or q / k themselves for bf16 in place).
+    """
+    dev = q.device
+    if q.dtype not in _ROPE_TYPES:
+        raise ValueError("q must be bf16, fp16 or fp32")
+    unit = 4 if q.dtype == torch.float32 else 8
+    _check_rows("q", q, (q.dtype,), unit, dev)
+    _check_stream(stream, dev)
+    B, N, H, d = q.shape
+    if plan.d != d:
+        raise ValueError(f"the plan is for head dimension {plan.d}, q has {d}")
+    a = _RopeArgs()
+    Hk = 0
+    if k is not None:
+        _check_rows("k", k, (q.dtype,), unit, dev)
+        Hk = k.shape[2]
+        if k.shape[:2] != q.shape[:2] or k.shape[3] != d:
+            raise ValueError("q [B, N, H, d] and k [B, N, Hk, d] must agree in B, N and d")
+    if (pos is None) == (grid is None):
+        raise ValueError("give either grid or pos")
+    axes = len(plan.dims)
+    if pos is None:
+        grid = [int(x) for x in grid]
+        if len(grid) != axes or any(not 0 < x < 1 << 63 for x in grid):
+            raise ValueError(f"grid: {axes} positive sizes")
+        if not 0 <= start <= math.prod(grid) - N:
+            raise ValueError("tokens start .. start + N - 1 must lie in the grid")
+        cells = (_I64 * axes)(*grid)
+        a.grid, a.start = ctypes.addressof(cells), int(start)
+    else:
+        if start:
+            raise ValueError("start belongs to grid")
+        if (pos.dtype not in (torch.float32, torch.int32) or pos.device != dev or not pos.is_contiguous()
+                or tuple(pos.shape) not in ((axes, N), (1, axes, N), (B, axes, N))):
+            raise ValueError(f"pos must be a contiguous fp32 or int32 tensor [{axes}, N] or [B, {axes}, N] on the device of q")
+        a.pos, a.pos_dtype = pos.data_ptr(), LITE_FP32 if pos.dtype == torch.float32 else LITE_INT32
+        a.pos_axis_stride, a.pos_batch_stride = N, axes * N if pos.dim() == 3 and pos.shape[0] > 1 else 0
+    if k is not None and (q_weight is None) != (k_weight is None):
+        raise ValueError("q_weight and k_weight go together")
+    if k is None and (k_weight is not None or k_out is not None):
+        raise ValueError("k_weight and k_out need k")
+    if q_weight is not None:
+        _check_weight("q_weight", q_weight, (d, H * d), dev)
+        rows = q_weight.numel() != d
+        if k is not None:
+            _check_weight("k_weight", k_weight, (d, Hk * d), dev)
+            if H > 1 and Hk > 1 and rows != (k_weight.numel() != d):
+                raise ValueError("q_weight and k_weight must both be per head or both per row")
+            # with one head the two norms are the same: the other tensor decides
+            rows = rows or k_weight.numel() != d
+            if rows and (q_weight.numel() != H * d or k_weight.numel() != Hk * d):
+                raise ValueError("q_weight and k_weight must both be per head or both per row")
+        a.norm, a.eps = 2 if rows else 1, float(eps)
+        if not (a.eps >= 0.0 and math.isfinite(a.eps)):
+            raise ValueError("eps must be a non-negative number")
+        a.q_weight = q_weight.data_ptr()
+        a.k_weight = None if k is None else k_weight.data_ptr()
+    if q_out is None:
+        q_out = _new((B, N, H, d), torch.bfloat16, dev, stream)
+    else:
+        _check_rows("q_out", q_out, (torch.bfloat16,), 8, dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    a.q, a.q_out, a.q_stride, a.q_out_stride = q.data_ptr(), q_out.data_ptr(), _strides(q), _strides(q_out)
+    if k is not None:
+        if k_out is None:
+            k_out = _new((B, N, Hk, d), torch.bfloat16, dev, stream)
+        else:
+            _check_rows("k_out", k_out, (torch.bfloat16,), 8, dev)
+            if k_out.shape != k.shape:
+                raise ValueError("k_out must have k's shape")
+        a.k, a.k_out, a.k_stride, a.k_out_stride = k.data_ptr(), k_out.data_ptr(), _strides(k), _strides(k_out)
+    a.freq, a.axis, a.n_axes = ctypes.addressof(plan._freq), ctypes.addressof(plan._axis), axes
+    a.dtype, a.pairing = _ROPE_TYPES[q.dtype], int(plan.pairing == "half")
+    a.B, a.N, a.H, a.Hk, a.d = B, N, H, Hk, d
+    _call_on("lite_qk_rope", a, dev, stream)
+    return q_out, k_out
+
+
+def _span_call(fn: str, q, k, v, k_prefix, v_prefix, spans, scale, cap, slopes, q_pos, k_pos, prefix_pos, o, lse,
+               return_lse, stream):
+    dev = q.device
+    bf16 = (torch.bfloat16,)
+    _check_rows("q", q, bf16, 8, dev, batch_zero=True)
+    _check_rows("k", k, bf16, 8, dev, batch_zero=True)
+    _check_rows("v", v, bf16, 8, dev, batch_zero=True)
+    _check_stream(stream, dev)
+    B, Nq, H, d = q.shape
+    Nk, Hk = k.shape[1], k.shape[2]
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != d:
+        raise ValueError("q [B, Nq, H, d] and k, v [B, Nk, Hk, d] must agree in B and d, k and v in shape")
+    if Hk == 0 or H % Hk:
+        raise ValueError("the heads of k must divide the heads of q")
+    a = _SpanArgs()
+    a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
+    a.q_stride, a.k_stride, a.v_stride = _strides(q), _strides(k), _strides(v)
+    Np = 0
+    if k_prefix is not None:
+        if k_prefix.dim() == 3 and v_prefix.dim() == 3:
+            k_prefix, v_prefix = k_prefix[None], v_prefix[None]
+        _check_rows("k_prefix", k_prefix, bf16, 8, dev)
+        _check_rows("v_prefix", v_prefix, bf16, 8, dev)
+        Np = k_prefix.shape[1]
+        if k_prefix.shape != v_prefix.shape or tuple(k_prefix.shape) != (1, Np, Hk, d):
+            raise ValueError("k_prefix and v_prefix must be [Np, Hk, d] with the heads and head dimension of k")
+        a.k_prefix, a.v_prefix = k_prefix.data_ptr(), v_prefix.data_ptr()
+        a.k_prefix_stride, a.v_prefix_stride = _strides(k_prefix), _strides(v_prefix)
+    if spans is not None:
+        if (spans.dtype != torch.int32 or spans.device != dev or not spans.is_contiguous()
+                or tuple(spans.shape) not in ((Nq, 2), (1, Nq, 2), (B, Nq, 2))):
+            raise ValueError("spans must be a contiguous int32 tensor [Nq, 2] or [B, Nq, 2] on the device of q")
+        a.spans, a.span_batches = spans.data_ptr(), spans.shape[0] if spans.dim() == 3 else 1
+    cap = float(cap or 0.0)
+    if not 0.0 <= cap < math.inf:
+        raise ValueError("cap must be a non-negative number (0: no cap)")
+    a.cap, a.scale = cap, float(scale or 0.0)
+    a.pos_batches = 1
+    if slopes is not None:
+        if slopes.dtype != torch.float32 or not slopes.is_contiguous() or slopes.device != dev or tuple(slopes.shape) != (H,):
+            raise ValueError("slopes must be a contiguous fp32 tensor [H] on the device of q")
+        a.slopes = slopes.data_ptr()
+        for name, t, n in (("q_pos", q_pos, Nq), ("k_pos", k_pos, Nk)):
+            if t is None:
+                continue
+            if (t.dtype != torch.float32 or not t.is_contiguous() or t.device != dev
+                    or tuple(t.shape) not in ((n,), (1, n), (B, n))):
+                raise ValueError(f"{name} must be a contiguous fp32 tensor [N] or [B, N] on the device of q")
+            batches = t.shape[0] if t.dim() == 2 else 1
+            if q_pos is not None and k_pos is not None and batches != (q_pos.shape[0] if q_pos.dim() == 2 else 1):
+                raise ValueError("q_pos and k_pos must both be for one or both for all batch entries")
+            a.pos_batches = batches
+            setattr(a, name, t.data_ptr())
+        if prefix_pos is not None:
+            if (prefix_pos.dtype != torch.float32 or not prefix_pos.is_contiguous() or prefix_pos.device != dev
+                    or tuple(prefix_pos.shape) != (Np,)):
+                raise ValueError("prefix_pos must be a contiguous fp32 tensor [Np] on the device of q")
+            a.prefix_pos = prefix_pos.data_ptr()
+    elif q_pos is not None or k_pos is not None or prefix_pos is not None:
+        raise ValueError("positions belong to slopes")
+    if o is None:
+        o = _new((B, Nq, H, d), torch.bfloat16, dev, stream)
+    if lse is None and return_lse:
+        lse = _new((B, H, Nq), torch.float32, dev, stream)
+    _check_outputs(q, o, lse)
+    a.o, a.lse = o.data_ptr(), _ptr(lse)
+    a.B, a.Nq, a.Nk, a.Np, a.H, a.Hk, a.d = B, Nq, Nk, Np, H, Hk, d
+    _call_on(fn, a, dev, stream)
+    return o, lse
+
+
+def lite_attn_span(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, spans: Optional[torch.Tensor] = None,
+                   scale: Optional[float] = None, cap: float = 0.0, slopes: Optional[torch.Tensor] = None,
+                   q_pos: Optional[torch.Tensor] = None, k_pos: Optional[torch.Tensor] = None,
+                   o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, return_lse: bool = True,
+                   stream=None):
+    """Attention of q [B, Nq, H, d] over k, v [B, Nk, Hk, d] in which row n sees the keys spans[.., n, 0]
+    <= m < spans[.., n, 1] (int32 [Nq, 2] or [B, Nq, 2]; None: all; spans.py makes the usual tables),
+    with scores capped by cap * tanh(s / cap) and lowered by slopes[h] * |q_pos - k_pos| where given
+    (see include/lite_attn.h). q, k and v may be strided views. Returns (o, lse or None)."""
+    return _span_call("lite_attn_span", q, k, v, None, None, spans, scale, cap, slopes, q_pos, k_pos, None, o, lse,
+                      return_lse, stream)
+
+
+def lite_attn_prefix(q: torch.Tensor, k_prefix: torch.Tensor, v_prefix: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     spans: Optional[torch.Tensor] = None, scale: Optional[float] = None, cap: float = 0.0,
+                     slopes: Optional[torch.Tensor] = None, q_pos: Optional[torch.Tensor] = None,
+                     k_pos: Optional[torch.Tensor] = None, prefix_pos: Optional[torch.Tensor] = None,
+                     o: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None, return_lse: bool = True,
+                     stream=None):
+    """lite_attn_span for a batch whose sequences share a prefix: every row also sees all keys of
+    k_prefix, v_prefix [Np, Hk, d], which are stored, and where rows are few read, once for the batch.
+    spans counts the own keys k, v [B, Nk, Hk, d]. Np or Nk may be 0. Returns (o, lse or None)."""
+    return _span_call("lite_attn_prefix", q, k, v, k_prefix, v_prefix, spans, scale, cap, slopes, q_pos, k_pos,
+                      prefix_pos, o, lse, return_lse, stream)
