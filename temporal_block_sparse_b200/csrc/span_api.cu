@@ -130,115 +130,174 @@ int check_attention(const lite_span_args& a, bool prefix) {
   return LITE_OK;
 }
 
-// How the work is split into items.
-struct Plan {
-  bool stacked;              // a prefix pass over tokens of the whole batch, then the own pass
-  int pre_pairs, pre_splits, own_pairs, own_splits;
-  int64_t n_items;
-  bool parts;
-};
-
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-Plan make_plan(const lite_span_args& a, int Np, int TN, int Tp, int Tk, int64_t slots) {
-  Plan pl;
-  std::memset(&pl, 0, sizeof(pl));
-  const int64_t tq_own = ceil_div(a.Nq, TN), tq_pre = ceil_div(int64_t(a.B) * a.Nq, TN);
-  const bool flat = a.B == 1 || a.Nq == 1 || a.q_stride[0] == int64_t(a.Nq) * a.q_stride[1];
-  // Stacking the batch's tokens into common tiles pays where it saves a quarter of the prefix pass
-  // or more; it costs a second pass over the parts.
-  pl.stacked = Np > 0 && a.B > 1 && flat && a.q_stride[0] > 0 && tq_pre * 4 <= a.B * tq_own * 3;
-  int64_t items_p = 0, items_o = 0, tiles_o = Tk;
-  if (pl.stacked) {
-    pl.pre_pairs = int(ceil_div(tq_pre, 2));
-    items_p = int64_t(a.Hk) * pl.pre_pairs;
-    pl.own_pairs = a.Nk > 0 ? int(ceil_div(tq_own, 2)) : 0;
-  } else {
-    pl.own_pairs = int(ceil_div(tq_own, 2));
-    tiles_o += Tp;
-  }
-  items_o = int64_t(a.B) * a.Hk * pl.own_pairs;
-  pl.pre_splits = pl.own_splits = 1;
-  // Few items leave SMs idle: their key ranges are split so that the longest CTA's work (items it
-  // takes, each t tiles and about two more for its start and its end) is shortest.
-  if (items_p + items_o < slots) {
-    const int64_t longest = std::max<int64_t>(pl.stacked ? Tp : 0, items_o ? tiles_o : 0);
-    int64_t best = INT64_MAX;
-    for (int64_t s = 1; s <= 128 && s <= longest; ++s) {
-      const int64_t t = ceil_div(longest, s);
-      const int64_t sp = items_p ? ceil_div(Tp, t) : 1, so = items_o ? std::max<int64_t>(1, ceil_div(tiles_o, t)) : 1;
-      const int64_t n = items_p * sp + items_o * so;
-      if (n > 2 * slots) break;
-      const int64_t cost = ceil_div(n, slots) * (t + 2) + ((sp > 1 || so > 1 || pl.stacked) ? 3 : 0);
-      if (cost < best) {
-        best = cost;
-        pl.pre_splits = int(sp);
-        pl.own_splits = int(so);
-      }
-    }
-  }
-  pl.n_items = items_p * pl.pre_splits + items_o * pl.own_splits;
-  pl.parts = pl.stacked || pl.own_splits > 1;
-  return pl;
+// One pass over query tiles (see SpanPass): `units` key heads (times batch entries), each with
+// `tokens` tokens against `tiles` key tiles.
+struct PassPlan {
+  int64_t units = 0, pairs = 0, splits = 1, tiles = 0;
+  int TN = 0, F = 1, alt = 0;
+  int64_t items() const { return units * pairs * splits; }
+};
+
+struct Plan {
+  bool stacked = false;  // a prefix pass over tokens of the whole batch beside the own pass
+  PassPlan pre, own;
+  bool parts = false;
+  double us = 0.0;       // estimated time
+};
+
+PassPlan make_pass(int64_t units, int64_t tokens, int G, int64_t tiles) {
+  PassPlan ps;
+  ps.units = units;
+  ps.tiles = tiles;
+  // Up to 32 rows (tokens x grouped heads): four copies of the rows share the key columns (F = 4).
+  ps.F = tokens * G <= 32 ? 4 : 1;
+  ps.TN = (ps.F == 4 ? 32 : 128) / G;
+  const int64_t tq = ceil_div(tokens, ps.TN);
+  ps.alt = tq == 1;
+  ps.pairs = ceil_div(tq, ps.alt ? 1 : 2);
+  return ps;
 }
 
-bool g_span_smem[kMaxDevices][8];
+// Microseconds that one CTA takes for an item of t key tiles: its start and end, and each tile, as
+// measured on a B200 with all CTAs busy (a d = 64 tile has half the keys and shares its SM).
+double item_us(const PassPlan& ps, int d, int64_t t) {
+  const double tile = ps.F == 4 ? (d == 64 ? 0.75 : 1.4) : ps.alt ? (d == 64 ? 0.9 : 1.6) : (d == 64 ? 1.7 : 2.5);
+  return 3.0 + tile * double(t);
+}
+
+// Time of both passes' items on `slots` CTAs: whole waves where all items are alike, else the
+// bound of list scheduling.
+double plan_us(const Plan& pl, int d, int64_t slots) {
+  const int64_t np = pl.pre.items(), no = pl.own.items();
+  const double tp = np ? item_us(pl.pre, d, ceil_div(pl.pre.tiles, pl.pre.splits)) : 0.0;
+  const double to = no ? item_us(pl.own, d, ceil_div(pl.own.tiles, pl.own.splits)) : 0.0;
+  double us;
+  if (np == 0 || no == 0)
+    us = double(ceil_div(np + no, slots)) * std::max(tp, to);
+  else
+    us = std::max(std::max(tp, to), (double(np) * tp + double(no) * to) / double(slots) + std::max(tp, to) * 0.5);
+  return us + (pl.parts ? 5.0 : 0.0);  // the join: its launch and the parts' way through L2
+}
+
+// Splits the key ranges where that shortens the plan: few items leave SMs idle, and one long item
+// can outlast all others.
+void choose_splits(Plan& pl, int d, int64_t slots) {
+  pl.us = plan_us(pl, d, slots);
+  const Plan base = pl;
+  const int64_t longest = std::max(base.pre.tiles, base.own.tiles);
+  const int64_t most = std::max<int64_t>(base.pre.items() + base.own.items(), 0) + 4 * slots;
+  for (int64_t s = 2; s <= 256 && s <= longest; ++s) {
+    Plan c = base;
+    const int64_t t = ceil_div(longest, s);
+    c.pre.splits = std::max<int64_t>(1, ceil_div(c.pre.tiles, t));
+    c.own.splits = std::max<int64_t>(1, ceil_div(c.own.tiles, t));
+    c.parts = true;
+    if (c.pre.items() + c.own.items() > most) break;
+    c.us = plan_us(c, d, slots);
+    if (c.us < pl.us) pl = c;
+  }
+}
+
+Plan make_plan(const lite_span_args& a, int Np, int Tp, int Tk, int64_t slots) {
+  const int G = a.H / a.Hk;
+  Plan best;
+  best.own = make_pass(int64_t(a.B) * a.Hk, a.Nq, G, int64_t(Tp) + Tk);
+  choose_splits(best, a.d, slots);
+  // Tokens of several entries in one query tile: the batch's tokens have to be evenly spaced in q.
+  const bool flat = a.B > 1 && a.q_stride[0] > 0 && (a.Nq == 1 || a.q_stride[0] == int64_t(a.Nq) * a.q_stride[1]);
+  if (Np > 0 && flat) {
+    Plan c;
+    c.stacked = c.parts = true;
+    c.pre = make_pass(a.Hk, int64_t(a.B) * a.Nq, G, Tp);
+    if (a.Nk > 0) c.own = make_pass(int64_t(a.B) * a.Hk, a.Nq, G, Tk);
+    choose_splits(c, a.d, slots);
+    if (c.us < best.us) best = c;
+  }
+  // One tile and no join: both groups on it would need one (F = 4 joins them in the CTA).
+  if (!best.parts && best.own.F == 1) best.own.alt = 0;
+  return best;
+}
+
+bool g_span_smem[kMaxDevices][16];
 std::mutex g_span_mu;
 
-template <int D, int BN, int MOD>
-int launch_span(const lite_span_args& a, int Np, const DeviceContext& dc, lite::SpanParams p, const Plan& pl,
-                cudaStream_t stream) {
+struct Maps {
+  CUtensorMap q, q_stack, k, v, kp, vp;
+};
+
+template <int D, int BN, int MOD, int F>
+int launch_span(const DeviceContext& dc, const Maps& m, const lite::SpanParams& p, cudaStream_t stream) {
   using C = lite::SpanCfg<D, BN>;
   {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return LITE_ERR_CUDA;
     std::lock_guard<std::mutex> lk(g_span_mu);
-    bool& set = g_span_smem[dev][(D == 128 ? 4 : 0) + MOD];
+    bool& set = g_span_smem[dev][(D == 128 ? 8 : 0) + (F == 4 ? 4 : 0) + MOD];
     if (!set) {
-      if (cudaFuncSetAttribute(lite::lite_span_kernel<D, BN, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      if (cudaFuncSetAttribute(lite::lite_span_kernel<D, BN, MOD, F>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                C::SMEM_BYTES) != cudaSuccess)
         return LITE_ERR_CUDA;
       set = true;
     }
   }
-  CUtensorMap tq, tqp, tk, tv, tkp, tvp;
-  if (!q_map(dc, &tq, a.q, a.B, a.Nq, a.Hk, p.G, D, a.q_stride, p.TN)) return LITE_ERR_CUDA;
-  tqp = tq;
-  if (pl.stacked) {
-    int64_t st[3] = {0, a.Nq > 1 ? a.q_stride[1] : a.q_stride[0], a.q_stride[2]};
-    if (!q_map(dc, &tqp, a.q, 1, a.B * a.Nq, a.Hk, p.G, D, st, p.TN)) return LITE_ERR_CUDA;
-  }
-  if (a.Nk > 0 && (!kv_map(dc, &tk, a.k, a.B, a.Nk, a.Hk, D, a.k_stride, BN) ||
-                   !kv_map(dc, &tv, a.v, a.B, a.Nk, a.Hk, D, a.v_stride, BN)))
-    return LITE_ERR_CUDA;
-  if (Np > 0 && (!kv_map(dc, &tkp, a.k_prefix, 1, Np, a.Hk, D, a.k_prefix_stride, BN) ||
-                 !kv_map(dc, &tvp, a.v_prefix, 1, Np, a.Hk, D, a.v_prefix_stride, BN)))
-    return LITE_ERR_CUDA;
-  if (a.Nk == 0) tk = tkp, tv = tvp;  // never loaded from
-  if (Np == 0) tkp = tk, tvp = tv;
   int64_t grid = int64_t(dc.sms) * C::CTAS_PER_SM;
   if (dc.max_ctas > 0) grid = std::min<int64_t>(grid, dc.max_ctas);
-  grid = std::min(grid, pl.n_items);
-  lite::lite_span_kernel<D, BN, MOD>
-      <<<unsigned(grid), C::THREADS, C::SMEM_BYTES, stream>>>(tq, tqp, tk, tv, tkp, tvp, p);
-  if (cudaGetLastError() != cudaSuccess) return LITE_ERR_CUDA;
-  if (pl.parts) {
-    const int64_t threads = int64_t(a.B) * a.Nq * a.H * (D / 4);
-    lite::lite_span_combine_kernel<D><<<unsigned(ceil_div(threads, 256)), 256, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return LITE_ERR_CUDA;
-  }
-  return LITE_OK;
+  grid = std::min<int64_t>(grid, p.n_items);
+  lite::lite_span_kernel<D, BN, MOD, F>
+      <<<unsigned(grid), C::THREADS, C::SMEM_BYTES, stream>>>(m.q, m.q_stack, m.k, m.v, m.kp, m.vp, p);
+  return cudaGetLastError() == cudaSuccess ? LITE_OK : LITE_ERR_CUDA;
 }
 
-template <int D, int BN>
-int launch_span_mod(const lite_span_args& a, int Np, const DeviceContext& dc, const lite::SpanParams& p, const Plan& pl,
-                    cudaStream_t stream) {
-  switch ((a.cap > 0.f ? lite::kSpanCap : 0) | (a.slopes ? lite::kSpanBias : 0)) {
-    case 0: return launch_span<D, BN, 0>(a, Np, dc, p, pl, stream);
-    case 1: return launch_span<D, BN, 1>(a, Np, dc, p, pl, stream);
-    case 2: return launch_span<D, BN, 2>(a, Np, dc, p, pl, stream);
-    default: return launch_span<D, BN, 3>(a, Np, dc, p, pl, stream);
+template <int D, int BN, int F>
+int launch_span_mod(int mod, const DeviceContext& dc, const Maps& m, const lite::SpanParams& p, cudaStream_t stream) {
+  switch (mod) {
+    case 0: return launch_span<D, BN, 0, F>(dc, m, p, stream);
+    case 1: return launch_span<D, BN, 1, F>(dc, m, p, stream);
+    case 2: return launch_span<D, BN, 2, F>(dc, m, p, stream);
+    default: return launch_span<D, BN, 3, F>(dc, m, p, stream);
   }
+}
+
+int launch_span_any(int d, int F, int mod, const DeviceContext& dc, const Maps& m, const lite::SpanParams& p,
+                    cudaStream_t stream) {
+  if (d == 64)
+    return F == 4 ? launch_span_mod<64, 64, 4>(mod, dc, m, p, stream) : launch_span_mod<64, 64, 1>(mod, dc, m, p, stream);
+  return F == 4 ? launch_span_mod<128, 128, 4>(mod, dc, m, p, stream) : launch_span_mod<128, 128, 1>(mod, dc, m, p, stream);
+}
+
+bool make_maps(const lite_span_args& a, int Np, const DeviceContext& dc, const Plan& pl, Maps* m) {
+  const int t = tile_for(a.d), G = a.H / a.Hk;
+  const int tn = pl.own.items() ? pl.own.TN : pl.pre.TN;
+  if (!q_map(dc, &m->q, a.q, a.B, a.Nq, a.Hk, G, a.d, a.q_stride, tn)) return false;
+  m->q_stack = m->q;
+  if (pl.stacked) {
+    const int64_t st[3] = {0, a.Nq > 1 ? a.q_stride[1] : a.q_stride[0], a.q_stride[2]};
+    if (!q_map(dc, &m->q_stack, a.q, 1, a.B * a.Nq, a.Hk, G, a.d, st, pl.pre.TN)) return false;
+  }
+  if (a.Nk > 0 && (!kv_map(dc, &m->k, a.k, a.B, a.Nk, a.Hk, a.d, a.k_stride, t) ||
+                   !kv_map(dc, &m->v, a.v, a.B, a.Nk, a.Hk, a.d, a.v_stride, t)))
+    return false;
+  if (Np > 0 && (!kv_map(dc, &m->kp, a.k_prefix, 1, Np, a.Hk, a.d, a.k_prefix_stride, t) ||
+                 !kv_map(dc, &m->vp, a.v_prefix, 1, Np, a.Hk, a.d, a.v_prefix_stride, t)))
+    return false;
+  // a map without keys is never loaded from
+  if (a.Nk == 0) m->k = m->kp, m->v = m->vp;
+  if (Np == 0) m->kp = m->k, m->vp = m->v;
+  return true;
+}
+
+lite::SpanPass kernel_pass(const PassPlan& ps, int64_t slot0) {
+  lite::SpanPass k;
+  k.items = int(ps.items());
+  k.pairs = int(ps.pairs);
+  k.splits = int(ps.splits);
+  k.alt = ps.alt;
+  k.TN = ps.TN;
+  k.per_item = ps.F == 4 ? 1 : 2;
+  k.slot0 = int(slot0);
+  return k;
 }
 
 int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
@@ -246,6 +305,11 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   DeviceContext dc;
   if (lite_host::device_context(false, &dc) != LITE_OK) return LITE_ERR_CUDA;
   const int t = tile_for(a.d);
+  const int64_t slots = int64_t(dc.sms) * (a.d == 64 ? 2 : 1);
+  const int Tp = int(ceil_div(Np, t));
+  const Plan pl = make_plan(a, Np, Tp, int(ceil_div(a.Nk, t)), slots);
+  const int64_t items = pl.pre.items() + pl.own.items();
+  if (items > INT_MAX / 2) return LITE_ERR_UNSUPPORTED;
   lite::SpanParams p;
   std::memset(&p, 0, sizeof(p));
   p.B = a.B;
@@ -255,11 +319,7 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   p.Nq = a.Nq;
   p.Nk = a.Nk;
   p.Np = Np;
-  p.TN = 128 / p.G;
-  p.Tp = int(ceil_div(Np, t));
-  const int64_t slots = int64_t(dc.sms) * (a.d == 64 ? 2 : 1);
-  const Plan pl = make_plan(a, Np, p.TN, p.Tp, int(ceil_div(a.Nk, t)), slots);
-  if (pl.n_items > INT_MAX) return LITE_ERR_UNSUPPORTED;
+  p.Tp = Tp;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
   p.spans = a.spans;
@@ -277,22 +337,22 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   p.k_bm = a.B > 1 && a.k_stride[0] != 0;
   p.v_bm = a.B > 1 && a.v_stride[0] != 0;
   p.fused = !pl.stacked;
-  p.pre_pairs = pl.pre_pairs;
-  p.pre_splits = pl.pre_splits;
-  p.own_pairs = pl.own_pairs;
-  p.own_splits = pl.own_splits;
-  p.pre_items = a.Hk * pl.pre_pairs * pl.pre_splits;
-  p.n_items = int(pl.n_items);
+  p.pre = kernel_pass(pl.pre, 0);
+  p.own = kernel_pass(pl.own, pl.pre.items() * p.pre.per_item);
   const float scale = (a.scale > 0.f && !std::isnan(a.scale)) ? a.scale : 1.0f / std::sqrt(float(a.d));
   p.scale_log2 = scale * 1.4426950408889634f;
   if (a.cap > 0.f) {
     p.cap_a = 2.f * p.scale_log2 / a.cap;
     p.cap_c = a.cap * 1.4426950408889634f;
   }
-  // Scratch: a work counter where items of unequal length are handed out one by one, and the parts.
-  const bool counter = a.spans && pl.n_items > slots;
+  // Scratch: work counters where there are more items than CTAs (their lengths depend on the spans), and
+  // the parts.
+  const bool counter = items > slots;
   const size_t floats = a.d == 64 ? lite::SpanPart<64>::FLOATS : lite::SpanPart<128>::FLOATS;
-  const size_t bytes = (counter ? 256 : 0) + (pl.parts ? size_t(pl.n_items) * 2 * floats * sizeof(float) : 0);
+  const size_t n_parts = pl.parts ? size_t(pl.pre.items()) * p.pre.per_item + size_t(pl.own.items()) * p.own.per_item : 0;
+  const size_t bytes = (counter ? 256 : 0) + n_parts * floats * sizeof(float);
+  Maps m;
+  if (!make_maps(a, Np, dc, pl, &m)) return LITE_ERR_CUDA;
   char* ws = nullptr;
   if (bytes) {
     if (lite_host::device_context(true, &dc) != LITE_OK) return LITE_ERR_CUDA;
@@ -301,11 +361,34 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   int st = LITE_OK;
   if (counter) {
     p.work_counter = reinterpret_cast<int*>(ws);
-    if (cudaMemsetAsync(ws, 0, sizeof(int), stream) != cudaSuccess) st = LITE_ERR_CUDA;
+    if (cudaMemsetAsync(ws, 0, 2 * sizeof(int), stream) != cudaSuccess) st = LITE_ERR_CUDA;
   }
   if (pl.parts) p.part = reinterpret_cast<float*>(ws + (counter ? 256 : 0));
-  if (!st)
-    st = a.d == 64 ? launch_span_mod<64, 64>(a, Np, dc, p, pl, stream) : launch_span_mod<128, 128>(a, Np, dc, p, pl, stream);
+  const int mod = (a.cap > 0.f ? lite::kSpanCap : 0) | (a.slopes ? lite::kSpanBias : 0);
+  // passes of one kind share a launch
+  const bool two = p.pre.items && p.own.items && pl.pre.F != pl.own.F;
+  if (!st) {
+    lite::SpanParams l = p;
+    if (two) l.own.items = 0;
+    l.n_items = l.pre.items + l.own.items;
+    st = launch_span_any(a.d, p.pre.items ? pl.pre.F : pl.own.F, mod, dc, m, l, stream);
+  }
+  if (!st && two) {
+    lite::SpanParams l = p;
+    l.pre.items = 0;
+    l.n_items = l.own.items;
+    if (counter) l.work_counter = p.work_counter + 1;
+    st = launch_span_any(a.d, pl.own.F, mod, dc, m, l, stream);
+  }
+  if (!st && pl.parts) {
+    const int64_t threads = int64_t(a.B) * a.Nq * a.H * (a.d / 4);
+    const unsigned blocks = unsigned(ceil_div(threads, 256));
+    if (a.d == 64)
+      lite::lite_span_combine_kernel<64><<<blocks, 256, 0, stream>>>(p);
+    else
+      lite::lite_span_combine_kernel<128><<<blocks, 256, 0, stream>>>(p);
+    if (cudaGetLastError() != cudaSuccess) st = LITE_ERR_CUDA;
+  }
   if (ws && cudaFreeAsync(ws, stream) != cudaSuccess && !st) st = LITE_ERR_CUDA;
   return st;
 }

@@ -41,6 +41,18 @@ __device__ __forceinline__ float fast_rcp(float x) {
 
 constexpr int kSpanCap = 1, kSpanBias = 2;  // MOD bits of the kernel
 
+// One pass over query tiles: the prefix pass (tokens of the whole batch against the shared prefix) or
+// the own pass (tokens of one batch entry against its keys).
+struct SpanPass {
+  int items;                // units * pairs * splits in this launch (units: Hk or B * Hk)
+  int pairs;                // work units of query tiles: pairs of tiles, or single tiles (alt)
+  int splits;               // parts of the key range
+  int alt;                  // both softmax groups take the one query tile, alternate key tiles
+  int TN;                   // tokens of a query tile: 128 / G, or 32 / G (F = 4)
+  int per_item;             // parts an item writes: 1 (F = 4) or 2
+  int slot0;                // index of the pass's first part
+};
+
 struct SpanParams {
   __nv_bfloat16* o;         // [B, Nq, H, D]
   float* lse;               // [B, H, Nq] or null
@@ -58,13 +70,10 @@ struct SpanParams {
   int debug_stall;
   int B, H, Hk, G, Nq, Nk, Np;
   int q_bm, k_bm, v_bm;     // 0: the tensor is the same for every batch entry, else 1
-  int TN;                   // tokens of a query tile: 128 / G
   int Tp;                   // prefix key tiles
   int fused;                // own items walk the prefix tiles too
-  int pre_pairs, pre_splits;  // prefix pass: tile pairs per key head (0: none), parts
-  int own_pairs, own_splits;  // own pass: tile pairs per (b, key head) (0: none), parts
-  int pre_items;            // Hk * pre_pairs * pre_splits
-  int n_items;              // + B * Hk * own_pairs * own_splits
+  SpanPass pre, own;
+  int n_items;              // pre.items + own.items of this launch
   float scale_log2;         // softmax scale * log2(e)
   float cap_a, cap_c;       // 2 scale log2(e) / cap and cap log2(e)
 };
@@ -75,20 +84,22 @@ struct SpanPart {
   static constexpr size_t FLOATS = 128 * D + 256;
 };
 
-// One query tile of an item: its live key tiles are n_pre prefix tiles from v_first on, then
-// n_live - n_pre own tiles from j_first on.
+// One query tile of an item. Its key tiles are list entries q = q0, q0 + step, .. (n_live of them): entry
+// q < n_pre is prefix tile v_first + q, the others own tile j_first + q - n_pre.
 struct SpanTile {
   int tok0;              // its first token (index in the pass: n, or b * Nq + n in the prefix pass)
   int rows;              // valid rows (0: the tile does not exist)
   int n_live, n_pre;
   int j_first;
+  int q0, step;
   int full_lo, full_hi;  // every row sees the own keys [full_lo, full_hi)
 };
 
 struct SpanInfo {
   int kind;              // -1 end of the work, 0 own pass, 1 prefix pass
+  int alt;
   int b, hk;
-  int item;              // index of its parts in scratch
+  int slot;              // index of its first part in scratch
   int v_first;
   SpanTile t[2];
 };
@@ -120,40 +131,33 @@ __device__ __forceinline__ void span_of(const SpanParams& p, int b, int n, int& 
 // Decodes item `idx` (whole warp; the result is in every lane).
 template <int BN>
 __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int lane, SpanInfo& it) {
-  int pair, split, splits, ntok;
-  it.item = idx;
-  if (idx < p.pre_items) {
-    it.kind = 1;
-    splits = p.pre_splits;
-    const int per = p.pre_pairs * splits;
-    it.hk = idx / per;
-    const int rem = idx - it.hk * per;
-    pair = rem / splits;
-    split = rem - pair * splits;
-    it.b = 0;
-    ntok = p.B * p.Nq;
-  } else {
-    it.kind = 0;
-    splits = p.own_splits;
-    const int i = idx - p.pre_items;
-    const int per = p.own_pairs * splits;
-    const int bh = i / per;
-    const int rem = i - bh * per;
-    // the last rows first: where rows see their past, these have the most keys
-    pair = p.own_pairs - 1 - rem / splits;
-    split = rem % splits;
-    it.b = bh / p.Hk;
-    it.hk = bh - it.b * p.Hk;
-    ntok = p.Nq;
-  }
-  const int tp = (it.kind == 1 || p.fused) ? p.Tp : 0;
+  const bool prefix = idx < p.pre.items;
+  const SpanPass& ps = prefix ? p.pre : p.own;
+  const int i = prefix ? idx : idx - p.pre.items;
+  const int per = ps.pairs * ps.splits, unit = i / per, rem = i - unit * per;
+  const int split = rem % ps.splits;
+  // the last rows first: where rows see their past, these have the most keys
+  const int pair = ps.pairs - 1 - rem / ps.splits;
+  it.kind = prefix ? 1 : 0;
+  it.alt = ps.alt;
+  it.b = prefix ? 0 : unit / p.Hk;
+  it.hk = prefix ? unit : unit - it.b * p.Hk;
+  it.slot = ps.slot0 + i * ps.per_item;
+  const int ntok = prefix ? p.B * p.Nq : p.Nq;
+  const int tp = (prefix || p.fused) ? p.Tp : 0;
   int jlo = 0x7fffffff, jhi = 0;  // own key tiles that either query tile has to see
   int tlo[2], thi[2];             // and each of them
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     SpanTile& t = it.t[g];
-    t.tok0 = (2 * pair + g) * p.TN;
-    const int toks = max(0, min(p.TN, ntok - t.tok0));
+    if (ps.alt && g == 1) {
+      it.t[1] = it.t[0];
+      tlo[1] = tlo[0];
+      thi[1] = thi[0];
+      break;
+    }
+    t.tok0 = (ps.alt ? pair : 2 * pair + g) * ps.TN;
+    const int toks = max(0, min(ps.TN, ntok - t.tok0));
     t.rows = toks * p.G;
     tlo[g] = thi[g] = 0;
     t.full_lo = 0;
@@ -192,7 +196,7 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
   if (jhi == 0) jlo = 0;
   // virtual tiles: prefix [0, tp), then own jlo .. jhi; this split's are [v0, v1)
   const long long total = tp + (jhi - jlo);
-  const int v0 = int(total * split / splits), v1 = int(total * (split + 1) / splits);
+  const int v0 = int(total * split / ps.splits), v1 = int(total * (split + 1) / ps.splits);
   it.v_first = v0;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
@@ -201,6 +205,9 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
     const int j0 = max(tlo[g], jlo + max(v0 - tp, 0)), j1 = min(thi[g], jlo + v1 - tp);
     t.j_first = j0;
     t.n_live = t.n_pre + (t.rows ? max(0, j1 - j0) : 0);
+    t.q0 = ps.alt ? g : 0;
+    t.step = ps.alt ? 2 : 1;
+    if (ps.alt) t.n_live = (t.n_live + 1 - g) >> 1;
   }
 }
 
@@ -216,13 +223,26 @@ struct SpanCfg : AttnCfg<D, BN> {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
-template <int D, int BN, int MOD>
+constexpr uint32_t kSpanAlt = 2048u;  // ring word: both groups use the first query tile
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+template <int D, int BN, int MOD, int F>
 __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
     lite_span_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQp,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
                      const SpanParams p) {
   using C = SpanCfg<D, BN>;
+  constexpr int NC = BN / F;  // key columns of a thread
   constexpr bool CAP = (MOD & kSpanCap) != 0, BIAS = (MOD & kSpanBias) != 0;
   static_assert(sizeof(SpanCtl) <= C::CTL_BYTES, "control block");
   // key positions of two tiles per warpgroup share the group's staging area
@@ -296,7 +316,6 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       ++u;
       return true;
     };
-    const uint32_t q_rows = uint32_t(p.TN * p.G);
     while (true) {
       const int slot = items & 1;
       int item = -1;
@@ -325,32 +344,45 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
         } else {
           if (qn >= 1) ok = wt.wait(BAR(q_empty), (qn - 1) & 1);
           if (ok) {
-            const uint32_t qtx = q_rows * 128u * C::NCHUNK;
-            ptx::mbar_arrive_expect_tx(BAR(q_full), (n0 > 0 ? qtx : 0u) + (n1 > 0 ? qtx : 0u));
-            for (int g = 0; g < 2; ++g)
+            // alternating groups share one Q tile; with F = 4 its rows go to all four quarters of it
+            const int n_q = it.alt ? 1 : 2;
+            const SpanPass& ps = it.kind == 1 ? p.pre : p.own;
+            const uint32_t qtx = uint32_t(ps.TN * p.G) * 128u * C::NCHUNK * F;
+            ptx::mbar_arrive_expect_tx(BAR(q_full), (n0 > 0 ? qtx : 0u) + (n_q > 1 && n1 > 0 ? qtx : 0u));
+            for (int g = 0; g < n_q; ++g)
               if ((g ? n1 : n0) > 0)
                 for (int c = 0; c < C::NCHUNK; ++c)
-                  ptx::tma_load_5d(sQ + g * C::Q_BYTES + c * C::Q_CHUNK, it.kind == 1 ? &tmQp : &tmQ, BAR(q_full),
-                                   c * 64, 0, it.t[g].tok0, it.hk, it.kind == 1 ? 0 : it.b * p.q_bm);
+                  for (int x = 0; x < F; ++x)
+                    ptx::tma_load_5d(sQ + g * C::Q_BYTES + c * C::Q_CHUNK + x * 4096, it.kind == 1 ? &tmQp : &tmQ,
+                                     BAR(q_full), c * 64, 0, it.t[g].tok0, it.hk, it.kind == 1 ? 0 : it.b * p.q_bm);
             q_armed = true;
             q_par = qn & 1;
-            const uint32_t item_bits = ((qn & 1) ? kItemOdd : 0u) | (qn >= 1 ? kItemAfterFirst : 0u);
+            const uint32_t item_bits =
+                ((qn & 1) ? kItemOdd : 0u) | (qn >= 1 ? kItemAfterFirst : 0u) | (it.alt ? kSpanAlt : 0u);
             uint32_t f = kItemFirst;
             // the union of the two tiles' key tiles: prefix tiles (common to both), then own ones in order
             int d0 = 0, d1 = 0;
             while (ok && (d0 < n0 || d1 < n1)) {
-              const bool pre0 = d0 < it.t[0].n_pre, pre1 = d1 < it.t[1].n_pre;
               const int none = 0x7fffffff;
-              int c0 = none, c1 = none, j;
-              bool pre = pre0 || pre1;
-              if (pre) {
-                if (pre0) c0 = it.v_first + d0;
-                if (pre1) c1 = it.v_first + d1;
+              int c0 = none, c1 = none;
+              bool pre;
+              if (it.alt) {
+                // entries in order, the groups in turn
+                const int q = d0 + d1;
+                pre = q < it.t[0].n_pre;
+                (d0 == d1 ? c0 : c1) = pre ? it.v_first + q : it.t[0].j_first + q - it.t[0].n_pre;
               } else {
-                if (d0 < n0) c0 = it.t[0].j_first + d0 - it.t[0].n_pre;
-                if (d1 < n1) c1 = it.t[1].j_first + d1 - it.t[1].n_pre;
+                const bool pre0 = d0 < it.t[0].n_pre, pre1 = d1 < it.t[1].n_pre;
+                pre = pre0 || pre1;
+                if (pre) {
+                  if (pre0) c0 = it.v_first + d0;
+                  if (pre1) c1 = it.v_first + d1;
+                } else {
+                  if (d0 < n0) c0 = it.t[0].j_first + d0 - it.t[0].n_pre;
+                  if (d1 < n1) c1 = it.t[1].j_first + d1 - it.t[1].n_pre;
+                }
               }
-              j = min(c0, c1);
+              const int j = min(c0, c1);
               f |= item_bits;
               if (c0 == j) {
                 f |= kLive0 | (d0 == 0 ? kFirst0 : 0u) | (d0 == n0 - 1 ? kLast0 : 0u);
@@ -402,49 +434,56 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
         const uint32_t f = ctl->ring[u & 3];
         ptx::tc_fence_after();
         bool need_q = (f & kItemFirst) != 0u;
+        auto pv = [&](int g) -> bool {
+          if ((prev & (kFirst0 << g)) && (prev & kItemAfterFirst) &&
+              !wt.wait(BAR(o_free[g]), (prev & kItemOdd) ? 0u : 1u))
+            return false;
+          if (!wt.wait(BAR(p_full[g]), pc[g] & 1)) return false;
+          ++pc[g];
+          ptx::tc_fence_after();
+          const uint32_t p_tmem = tmem + C::S_COL + g * BN;
+          const uint32_t o_tmem = tmem + C::O_COL + g * D;
+          const uint64_t vd = v_desc0 + uint64_t((((u - 1) & 1) * C::KV_BYTES) >> 4);
+          const bool fresh = (prev & (kFirst0 << g)) != 0u;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          if (prev & (kLive0 << g)) {
-            if ((prev & (kFirst0 << g)) && (prev & kItemAfterFirst) &&
-                !wt.wait(BAR(o_free[g]), (prev & kItemOdd) ? 0u : 1u)) {
-              ok = false;
-              break;
-            }
-            if (!wt.wait(BAR(p_full[g]), pc[g] & 1)) {
-              ok = false;
-              break;
-            }
-            ++pc[g];
+          for (int kk = 0; kk < BN / 16; ++kk)
+            ptx::mma_ts(o_tmem, p_tmem + kk * 8, vd + uint64_t(kk * 128), C::IDESC_PV, (fresh && kk == 0) ? 0u : 1u);
+          if (prev & (kLast0 << g)) ptx::mma_commit(BAR(pv_done[g]));
+          return true;
+        };
+        auto qk = [&](int g) -> bool {
+          if (need_q) {
+            if (!wt.wait(BAR(q_full), (f & kItemOdd) ? 1u : 0u)) return false;
             ptx::tc_fence_after();
-            const uint32_t p_tmem = tmem + C::S_COL + g * BN;
-            const uint32_t o_tmem = tmem + C::O_COL + g * D;
-            const uint64_t vd = v_desc0 + uint64_t((((u - 1) & 1) * C::KV_BYTES) >> 4);
-            const bool fresh = (prev & (kFirst0 << g)) != 0u;
-#pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              ptx::mma_ts(o_tmem, p_tmem + kk * 8, vd + uint64_t(kk * 128), C::IDESC_PV, (fresh && kk == 0) ? 0u : 1u);
-            if (prev & (kLast0 << g)) ptx::mma_commit(BAR(pv_done[g]));
+            need_q = false;
           }
-          if (f & (kLive0 << g)) {
-            if (need_q) {
-              if (!wt.wait(BAR(q_full), (f & kItemOdd) ? 1u : 0u)) {
-                ok = false;
-                break;
-              }
-              ptx::tc_fence_after();
-              need_q = false;
-            }
-            const uint64_t qd = q_desc0 + uint64_t((g * C::Q_BYTES) >> 4);
-            const uint64_t kd = k_desc0 + uint64_t(((u & 1) * C::KV_BYTES) >> 4);
-            const uint32_t s_tmem = tmem + C::S_COL + g * BN;
+          const uint64_t qd = q_desc0 + uint64_t((((f & kSpanAlt) ? 0 : g) * C::Q_BYTES) >> 4);
+          const uint64_t kd = k_desc0 + uint64_t(((u & 1) * C::KV_BYTES) >> 4);
+          const uint32_t s_tmem = tmem + C::S_COL + g * BN;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = uint64_t((kk >> 2) * (C::Q_CHUNK >> 4) + (kk & 3) * 2);
-              const uint64_t offk = uint64_t((kk >> 2) * (C::KV_CHUNK >> 4) + (kk & 3) * 2);
-              ptx::mma_ss(s_tmem, qd + off, kd + offk, C::IDESC_QK, kk > 0 ? 1u : 0u);
-            }
-            ptx::mma_commit(BAR(s_full[g]));
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t off = uint64_t((kk >> 2) * (C::Q_CHUNK >> 4) + (kk & 3) * 2);
+            const uint64_t offk = uint64_t((kk >> 2) * (C::KV_CHUNK >> 4) + (kk & 3) * 2);
+            ptx::mma_ss(s_tmem, qd + off, kd + offk, C::IDESC_QK, kk > 0 ? 1u : 0u);
           }
+          ptx::mma_commit(BAR(s_full[g]));
+          return true;
+        };
+        if (prev & f & (kLive0 | kLive1)) {
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            if (ok && (prev & (kLive0 << g))) ok = pv(g);
+            if (ok && (f & (kLive0 << g))) ok = qk(g);
+          }
+        } else {
+          // The two tiles are for different groups (alternating ones above all): this tile's scores
+          // need not wait for the other group's softmax.
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            if (ok && (f & (kLive0 << g))) ok = qk(g);
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            if (ok && (prev & (kLive0 << g))) ok = pv(g);
         }
         if (!ok || (f & kEnd)) break;
         ptx::mma_commit(bar_free + (u & 1) * 8);
@@ -460,14 +499,17 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
     // ------------------------------------------------------------------------- softmax warpgroups
     const int grp = (warp - 2) >> 2;
     const int quarter = warp & 3;
-    const int r = quarter * 32 + lane;  // TMEM lane = row of the query tile
+    const int r = quarter * 32 + lane;       // TMEM lane
+    const int row = F == 1 ? r : lane;       // row of the query tile
+    const int col0 = F == 1 ? 0 : quarter * NC;  // this thread's first key column of a tile
     const uint32_t lane_base = uint32_t(quarter * 32) << 16;
     const uint32_t gbar = 1 + grp;
+    constexpr uint32_t kAll = 7;  // named barrier of both groups
     uint8_t* stage = smem + C::OFF_OST + (grp * 4 + quarter) * C::OST_WARP;
     float* kpos = reinterpret_cast<float*>(smem + C::OFF_OST + grp * 4 * C::OST_WARP);  // two tiles (bias)
     const uint32_t s_tmem = tmem + lane_base + C::S_COL + grp * BN;
     const uint32_t o_tmem = tmem + lane_base + C::O_COL + grp * D;
-    const int r_tok = r / p.G, r_head = r - r_tok * p.G;
+    const int r_tok = row / p.G, r_head = row - r_tok * p.G;
     // batch entry, token and head of this thread's row in the item
     auto row_of = [&](const SpanInfo* it, int& b, int& n, int& h) {
       b = it->b;
@@ -485,10 +527,11 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       const SpanInfo* it = &ctl->info[slot];  // released (item_empty) at the end of the item
       const SpanTile* mt = &it->t[grp];
       ++items;
-      if (!ptx::named_bar_and(gbar, 128, ok) || it->kind < 0) break;
+      // (with F > 1 the groups meet in the epilogue, so they give up together)
+      if (!ptx::named_bar_and(F > 1 ? kAll : gbar, F > 1 ? 256 : 128, ok) || it->kind < 0) break;
       const int n_live = mt->n_live;
-      const bool valid = r < mt->rows;
-      const bool warp_valid = quarter * 32 < mt->rows;  // the warp has a valid row
+      const bool valid = row < mt->rows;
+      const bool warp_valid = F > 1 || quarter * 32 < mt->rows;  // the warp has a valid row
       int ks = 0, ke = 0;
       float slope = 0.f, qp = 0.f;
       if (valid) {
@@ -503,8 +546,9 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       float m_used = -INFINITY;  // exponent reference (lazy rescale), log2 units
       float l = 0.f;             // row sum relative to m_used
       for (int idx = 0; idx < n_live; ++idx) {
-        const bool pre = idx < mt->n_pre;
-        const int j0 = (pre ? it->v_first + idx : mt->j_first + idx - mt->n_pre) * BN;  // the tile's first key
+        const int entry = mt->q0 + idx * mt->step;
+        const bool pre = entry < mt->n_pre;
+        const int j0 = (pre ? it->v_first + entry : mt->j_first + entry - mt->n_pre) * BN;  // the tile's first key
         float* kp = kpos + (idx & 1) * BN;
         if (BIAS) {
           // thread r brings the position of key r; the buffer's last readers passed the barrier of
@@ -526,24 +570,28 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
         __syncwarp();
         ptx::tc_fence_after();
         if (warp_valid) {
-          uint32_t sr[BN];
+          uint32_t sr[NC];
+          if constexpr (NC >= 32) {
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c)
-            ptx::tmem_ld32(s_tmem + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+            for (int c = 0; c < NC / 32; ++c)
+              ptx::tmem_ld32(s_tmem + col0 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
+          } else {
+            tmem_ld16(s_tmem + col0, sr);
+          }
           ptx::tmem_wait_ld();
-          float s[BN];
+          float s[NC];
 #pragma unroll
-          for (int x = 0; x < BN; ++x) s[x] = __uint_as_float(sr[x]);
+          for (int x = 0; x < NC; ++x) s[x] = __uint_as_float(sr[x]);
           if (CAP) {
             // cap tanh(z) = cap - 2 cap / (1 + e^{2z}), in log2 units; both ends saturate exactly
 #pragma unroll
-            for (int x = 0; x < BN; ++x)
+            for (int x = 0; x < NC; ++x)
               s[x] = fmaf(-2.f * p.cap_c, fast_rcp(1.f + ptx::ex2(s[x] * p.cap_a)), p.cap_c);
           }
           if (BIAS) {
 #pragma unroll
-            for (int x = 0; x < BN; x += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(kp + x);
+            for (int x = 0; x < NC; x += 4) {
+              const float4 k4 = *reinterpret_cast<const float4*>(kp + col0 + x);
               const float dd[4] = {k4.x - qp, k4.y - qp, k4.z - qp, k4.w - qp};
 #pragma unroll
               for (int y = 0; y < 4; ++y) {
@@ -558,19 +606,20 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           if (masked) {
             // each half-word of 32 columns as a bit mask, then one select per column
 #pragma unroll
-            for (int c = 0; c < BN / 32; ++c) {
-              const int a = min(max(lo - 32 * c, 0), 32), z = min(max(hi - 32 * c, 0), 32);
+            for (int c = 0; c < (NC + 31) / 32; ++c) {
+              const int at = col0 + 32 * c;
+              const int a = min(max(lo - at, 0), 32), z = min(max(hi - at, 0), 32);
               const uint32_t upto = z >= 32 ? 0xffffffffu : ((1u << z) - 1u);
               const uint32_t below = a >= 32 ? 0xffffffffu : ((1u << a) - 1u);
               const uint32_t bits = upto & ~below;
 #pragma unroll
-              for (int x = 0; x < 32; ++x)
+              for (int x = 0; x < (NC < 32 ? NC : 32); ++x)
                 s[32 * c + x] = (bits & (1u << x)) ? s[32 * c + x] : -INFINITY;
             }
           }
           float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
 #pragma unroll
-          for (int x = 0; x < BN; x += 8) {
+          for (int x = 0; x < NC; x += 8) {
             m0 = ptx::fmax3(m0, s[x], s[x + 1]);
             m1 = ptx::fmax3(m1, s[x + 2], s[x + 3]);
             m2 = ptx::fmax3(m2, s[x + 4], s[x + 5]);
@@ -590,19 +639,37 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           const float2 sc2 = make_float2(to_log2, to_log2);
           const float2 nm2 = make_float2(neg_m, neg_m);
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          constexpr int PC = NC < 32 ? NC : 32;  // columns converted and stored at a time
 #pragma unroll
-          for (int c = 0; c < BN / 32; ++c) {
-            uint32_t pk[16];
+          for (int c = 0; c < NC / PC; ++c) {
+            uint32_t pk[PC / 2];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float2 sx = make_float2(s[32 * c + 2 * x], s[32 * c + 2 * x + 1]);
+            for (int x = 0; x < PC / 2; ++x) {
+              const float2 sx = make_float2(s[PC * c + 2 * x], s[PC * c + 2 * x + 1]);
               const float2 a = MOD ? __fadd2_rn(sx, nm2) : __ffma2_rn(sx, sc2, nm2);
               const float2 pp = make_float2(ptx::ex2(a.x), ptx::ex2(a.y));
               acc[x & 3] = __fadd2_rn(acc[x & 3], pp);
               __nv_bfloat162 h2 = __floats2bfloat162_rn(pp.x, pp.y);
               pk[x] = *reinterpret_cast<uint32_t*>(&h2);
             }
-            ptx::tmem_st16(s_tmem + c * 16, pk);
+            if constexpr (PC == 32)
+              ptx::tmem_st16(s_tmem + col0 / 2 + c * 16, pk);
+            else
+              ptx::tmem_st8(s_tmem + col0 / 2, pk);
+          }
+          if constexpr (F > 1) {
+            // the other quarters of the row's keys are another lane's: P = 0 there
+            uint32_t zero[NC / 2];
+#pragma unroll
+            for (int x = 0; x < NC / 2; ++x) zero[x] = 0u;
+#pragma unroll
+            for (int c = 1; c < F; ++c) {
+              const uint32_t at = s_tmem + ((quarter + c) & (F - 1)) * (NC / 2);
+              if constexpr (NC == 32)
+                ptx::tmem_st16(at, zero);
+              else
+                ptx::tmem_st8(at, zero);
+            }
           }
           if (__any_sync(0xffffffffu, need) && idx >= 1) {
 #pragma unroll 1
@@ -623,7 +690,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
         ptx::mbar_arrive(BAR(p_full[grp]));
       }
       // ----- epilogue
-      if (BIAS) ptx::named_bar_sync(gbar, 128);  // the position buffer becomes the staging area
+      if (BIAS && F == 1) ptx::named_bar_sync(gbar, 128);  // the position buffer becomes the staging area
       if (n_live > 0) {
         wt.wait(BAR(pv_done[grp]), pv_phase & 1);
         ++pv_phase;
@@ -632,8 +699,80 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       }
       // a row that saw no key: o = 0, lse = -inf (l is 0 then; a NaN score leaves its mark in l)
       const bool empty = l == 0.f;
-      if (p.part) {
-        float* part = p.part + (size_t(it->item) * 2 + grp) * SpanPart<D>::FLOATS;
+      if constexpr (F > 1) {
+        // The row's eight partial results (four quarters, two groups) are joined here, 32 columns at a time
+        // through the staging area: thread x of the 256 takes row x / 8 and four columns of each 32.
+        float* ml = reinterpret_cast<float*>(smem + C::OFF_OST);
+        const int src = grp * 4 + quarter, x256 = grp * 128 + quarter * 32 + lane;
+        const int orow = x256 >> 3, quad = x256 & 7;
+        ptx::named_bar_sync(kAll, 256);
+        *reinterpret_cast<float2*>(ml + (src * 32 + lane) * 2) = make_float2(m_used, l);
+        ptx::named_bar_sync(kAll, 256);
+        float mm = -INFINITY, tot = 0.f, w[8];
+#pragma unroll
+        for (int y = 0; y < 8; ++y) mm = fmaxf(mm, ml[(y * 32 + orow) * 2]);
+#pragma unroll
+        for (int y = 0; y < 8; ++y) {
+          const float2 e = *reinterpret_cast<const float2*>(ml + (y * 32 + orow) * 2);
+          w[y] = e.y == 0.f ? 0.f : (mm == -INFINITY ? 1.f : ptx::ex2(e.x - mm));
+          if (e.y != 0.f) tot = fmaf(w[y], e.y, tot);
+        }
+        ptx::named_bar_sync(kAll, 256);
+        const bool o_valid = orow < mt->rows;
+        const float inv = p.part ? 1.f : (tot == 0.f ? 0.f : 1.f / tot);
+        int b = it->b, n = mt->tok0 + orow / p.G;
+        if (it->kind == 1) {
+          b = n / p.Nq;
+          n -= b * p.Nq;
+        }
+        const int h = it->hk * p.G + orow % p.G;
+        float* part = p.part + size_t(it->slot) * SpanPart<D>::FLOATS;
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t rr[32];
+          ptx::tmem_ld32(o_tmem + c * 32, rr);
+          ptx::tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) =
+                make_uint4(rr[4 * x], rr[4 * x + 1], rr[4 * x + 2], rr[4 * x + 3]);
+          ptx::named_bar_sync(kAll, 256);
+          float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int y = 0; y < 8; ++y) {
+            if (w[y] == 0.f) continue;
+            const float4 e = *reinterpret_cast<const float4*>(smem + C::OFF_OST + y * C::OST_WARP + orow * 128 +
+                                                              ((quad ^ (orow & 7)) << 4));
+            acc4.x = fmaf(w[y], e.x, acc4.x);
+            acc4.y = fmaf(w[y], e.y, acc4.y);
+            acc4.z = fmaf(w[y], e.z, acc4.z);
+            acc4.w = fmaf(w[y], e.w, acc4.w);
+          }
+          if (o_valid) {
+            if (p.part) {
+              *reinterpret_cast<float4*>(part + orow * D + c * 32 + quad * 4) = acc4;
+            } else {
+              const __nv_bfloat162 a = __floats2bfloat162_rn(acc4.x * inv, acc4.y * inv),
+                                   z = __floats2bfloat162_rn(acc4.z * inv, acc4.w * inv);
+              *reinterpret_cast<uint2*>(p.o + ((static_cast<long long>(b) * p.Nq + n) * p.H + h) * D + c * 32 + quad * 4) =
+                  make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&z));
+            }
+          }
+          ptx::named_bar_sync(kAll, 256);
+        }
+        ptx::tc_fence_before();
+        if (it->t[0].n_live + it->t[1].n_live > 0) ptx::mbar_arrive(BAR(o_free[grp]));
+        if (o_valid && quad == 0) {
+          if (p.part) {
+            part[128 * D + orow] = mm;
+            part[128 * D + 128 + orow] = tot;
+          } else if (p.lse) {
+            p.lse[(size_t(b) * p.H + h) * p.Nq + n] =
+                tot == 0.f ? -INFINITY : (mm + __log2f(tot)) * 0.6931471805599453f;
+          }
+        }
+      } else if (p.part) {
+        float* part = p.part + size_t(it->slot + grp) * SpanPart<D>::FLOATS;
         if (warp_valid) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -729,32 +868,33 @@ __global__ void __launch_bounds__(256) lite_span_combine_kernel(const SpanParams
   const long long bn = row / p.H;
   const int b = int(bn / p.Nq), n = int(bn - static_cast<long long>(b) * p.Nq);
   const int hk = h / p.G, gh = h - hk * p.G;
-  const float* part[2] = {nullptr, nullptr};
-  int count[2] = {0, 0}, at[2] = {0, 0};
-  if (p.pre_pairs) {
-    const int tok = int(bn), tile = tok / p.TN;
-    at[0] = (tok - tile * p.TN) * p.G + gh;
-    part[0] = p.part + (size_t(hk * p.pre_pairs + (tile >> 1)) * p.pre_splits * 2 + (tile & 1)) * SpanPart<D>::FLOATS;
-    count[0] = p.pre_splits;
+  const float* part[2];
+  int count[2], at[2];
+  size_t step[2];  // from one part of the row to the next
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const SpanPass& ps = k ? p.own : p.pre;
+    count[k] = 0;
+    if (ps.pairs == 0) continue;
+    const int tok = k ? n : int(bn), tile = tok / ps.TN;
+    at[k] = (tok - tile * ps.TN) * p.G + gh;
+    const int pair = ps.alt ? tile : tile >> 1, unit = k ? b * p.Hk + hk : hk;
+    const size_t first = ps.slot0 + (size_t(unit) * ps.pairs + (ps.pairs - 1 - pair)) * ps.splits * ps.per_item;
+    part[k] = p.part + (first + (ps.alt ? 0 : tile & 1)) * SpanPart<D>::FLOATS;
+    // alternating groups: every part of the item holds the row
+    count[k] = ps.alt ? ps.splits * ps.per_item : ps.splits;
+    step[k] = (ps.alt ? 1 : ps.per_item) * SpanPart<D>::FLOATS;
   }
-  if (p.own_pairs) {
-    const int tile = n / p.TN;
-    at[1] = (n - tile * p.TN) * p.G + gh;
-    const size_t item = p.pre_items + (size_t(b * p.Hk + hk) * p.own_pairs + (p.own_pairs - 1 - (tile >> 1))) * p.own_splits;
-    part[1] = p.part + (item * 2 + (tile & 1)) * SpanPart<D>::FLOATS;
-    count[1] = p.own_splits;
-  }
-  constexpr size_t STEP = 2 * SpanPart<D>::FLOATS;  // from one split's part to the next's
   float m = -INFINITY;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
-    for (int i = 0; i < count[k]; ++i) m = fmaxf(m, part[k][i * STEP + 128 * D + at[k]]);
+    for (int i = 0; i < count[k]; ++i) m = fmaxf(m, part[k][i * step[k] + 128 * D + at[k]]);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float tot = 0.f;
 #pragma unroll
   for (int k = 0; k < 2; ++k)
     for (int i = 0; i < count[k]; ++i) {
-      const float* q = part[k] + i * STEP;
+      const float* q = part[k] + i * step[k];
       const float mi = q[128 * D + at[k]], li = q[128 * D + 128 + at[k]];
       if (li == 0.f) continue;  // the part saw no key
       const float w = m == -INFINITY ? 1.f : exp2f(mi - m);
