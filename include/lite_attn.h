@@ -398,8 +398,8 @@ int lite_dropped_mass(const float* lse_live, const float* lse_full, float* row_m
  *                 NULL: token n is cell start + n of the row-major grid grid[0] x .. x
  *                 grid[n_axes - 1] (HOST), its positions are the cell's coordinates; start + N may not
  *                 exceed the number of cells.
- *  The host arrays are read during the call only. d in {64, 128}; (H + Hk) * d <= 32768;
- *  B * N < 2^31 - 1024. No scratch.
+ *  The host arrays are read during the call only. d in {64, 128}; H * d, Hk * d <= 16384;
+ *  B * N <= 2^30. No scratch.
  */
 enum { LITE_BF16 = 0, LITE_FP16 = 1, LITE_FP32 = 2, LITE_INT32 = 3 };
 typedef struct lite_rope_args {

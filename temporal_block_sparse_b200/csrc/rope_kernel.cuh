@@ -8,17 +8,22 @@
 // with (x0, x1) = elements (2p, 2p+1) (interleaved) or (p, p + d/2) (halves).
 //
 // HBM-bound: every element is read once and written once; the weights and the angles of a token are
-// shared by all its heads. A thread's unit is 16 elements of one head, the 8-element chunks c and
-// c + d/16: with halves these hold both elements of 8 pairs, with interleaved pairs they are
-// complete by themselves, so one mapping serves both and the d/16 lanes of a head read whole
-// 64- or 128-byte pieces. A block takes whole tokens (one, or several when a token has few heads).
-// All of a thread's loads are issued before anything else, so that the position arithmetic and
-// both barriers run under their latency.
+// shared by all its heads. A thread's unit is 16 elements of one head in 16-byte pieces (two of bf16 or fp16,
+// four of fp32): piece j of lane c holds elements j * d / pieces + c * (elements of a piece) and on, so the
+// d/16 lanes of a head read and write whole 32-byte sectors side by side, interleaved pairs lie
+// within a piece, and with halves piece j pairs with piece j + pieces / 2. Blocks are persistent, each
+// for queries or for keys, and take whole tokens (one, or several when a token has few heads); a
+// thread keeps its place in the token, so that little index arithmetic is left in the loop. The data
+// of the next tokens come in by asynchronous copies (each thread copies what it will read itself, so they
+// need no barrier), and their angles are computed beside the present work: one barrier per step is
+// left (none, but for new angles, without a row norm), and the loads never stop.
 //
-// The angle is formed in 64 bits as turns, position * (f / 2 pi), and reduced to [-1/2, 1/2] before
-// it becomes a 32-bit number: positions of a long stream reach 10^5 and more, where a 32-bit angle
-// is off by 10^-2. Sums of squares are 32-bit: a head's in its lanes' shuffle tree, a row's over
-// its heads in index order, the same on every run. The only rounding is the output's, to bf16.
+// Angles are formed in 64 bits and reduced to half a turn either way before they become 32-bit
+// numbers: positions of a long stream reach 10^5 and more, where a 32-bit angle is off by 10^-2. For whole
+// positions the turns of a pair are a 64-bit fraction, position * frequency / 2 pi modulo 1 being one
+// integer product that wraps; other positions take a product of doubles. cos and sin of the reduced
+// angle come from the special function unit (off by at most 2^-20.5, an output's rounding is
+// 2^-9 and more). Sums of squares are 32-bit, in a fixed order. The only rounding is the output's, to bf16.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -40,247 +45,365 @@ struct RopeTensor {
 };
 
 struct RopeParams {
-  RopeTensor t[2];        // queries, keys (heads = 0: no keys)
+  RopeTensor t[2];        // queries, keys
+  int q_blocks;           // blocks 0 .. q_blocks-1 take queries, the others keys
+  int halves;             // pairs (p, p + d/2) instead of (2p, 2p + 1)
   int tokens;             // B * N
   int N;
-  int units;              // units of one token: (heads[0] + heads[1]) * d / 16
-  int units_q;            // of which queries: heads[0] * d / 16
-  int tpb;                // tokens per block
-  int norm;               // 0 none, 1 over the head, 2 over the token's heads
+  uint64_t n_magic;       // floor(2^63 / N) + 1: t / N = (2 t n_magic) >> 64 for t < 2^31
   float eps;
   int n_axes;
   long long grid[kRopeMaxAxes];   // sizes of the token grid (pos == null), last axis fastest
   long long start;                // grid index of token 0
   const void* pos;                // [B or 1, axes, N] positions, or null
   int pos_is_int;
+  int whole;              // positions are whole numbers: grid or int32
   long long pos_b, pos_a;         // strides of pos in elements
-  double turns[kRopeMaxPairs];    // frequency / 2 pi of each pair
+  double turns[kRopeMaxPairs];    // frequency / 2 pi of each pair; its fractional part times 2^64 as an
+                                  // integer where positions are whole
   uint8_t axis[kRopeMaxPairs];
 };
 
-// 8 consecutive elements as floats
-struct Raw16 {
-  uint4 v;
-};
-struct Raw32 {
-  uint4 lo, hi;
-};
-template <typename T>
-struct RopeIn;
-template <>
-struct RopeIn<__nv_bfloat16> {
-  using Raw = Raw16;
-  static __device__ __forceinline__ Raw load(const __nv_bfloat16* p) {
-    return Raw{__ldcs(reinterpret_cast<const uint4*>(p))};
-  }
-  static __device__ __forceinline__ void get(const Raw& r, float (&f)[8]) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&r.v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 a = __bfloat1622float2(h[e]);
-      f[2 * e] = a.x;
-      f[2 * e + 1] = a.y;
-    }
-  }
-};
-template <>
-struct RopeIn<__half> {
-  using Raw = Raw16;
-  static __device__ __forceinline__ Raw load(const __half* p) {
-    return Raw{__ldcs(reinterpret_cast<const uint4*>(p))};
-  }
-  static __device__ __forceinline__ void get(const Raw& r, float (&f)[8]) {
-    const __half2* h = reinterpret_cast<const __half2*>(&r.v);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 a = __half22float2(h[e]);
-      f[2 * e] = a.x;
-      f[2 * e + 1] = a.y;
-    }
-  }
-};
-template <>
-struct RopeIn<float> {
-  using Raw = Raw32;
-  static __device__ __forceinline__ Raw load(const float* p) {
-    const uint4* q = reinterpret_cast<const uint4*>(p);
-    return Raw{__ldcs(q), __ldcs(q + 1)};
-  }
-  static __device__ __forceinline__ void get(const Raw& r, float (&f)[8]) {
-    const float* a = reinterpret_cast<const float*>(&r.lo);
-    const float* b = reinterpret_cast<const float*>(&r.hi);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f[e] = a[e];
-      f[4 + e] = b[e];
-    }
-  }
-};
+// The 16 bytes at `src` to shared memory, past the registers; complete after rope_copies_left().
+__device__ __forceinline__ void rope_copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void rope_copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// waits until at most N of this thread's committed groups are under way
+template <int N>
+__device__ __forceinline__ void rope_copies_left() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 
-__device__ __forceinline__ uint4 rope_pack(const float (&f)[8]) {
-  uint4 r;
-  uint32_t* o = reinterpret_cast<uint32_t*>(&r);
+// elements of one 16-byte piece, in pairs
+__device__ __forceinline__ void rope_get(const uint4& v, const __nv_bfloat16*, float2* f) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+  for (int e = 0; e < 4; ++e) f[e] = __bfloat1622float2(h[e]);
+}
+__device__ __forceinline__ void rope_get(const uint4& v, const __half*, float2* f) {
+  const __half2* h = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = __half22float2(h[e]);
+}
+__device__ __forceinline__ void rope_get(const uint4& v, const float*, float2* f) {
+  const float4 a = *reinterpret_cast<const float4*>(&v);
+  f[0] = make_float2(a.x, a.y);
+  f[1] = make_float2(a.z, a.w);
+}
+
+// N element pairs rounded to bf16 and stored (8 or 16 bytes)
+template <int N>
+__device__ __forceinline__ void rope_put(uint8_t* dst, const float2* f) {
+  uint32_t o[N];
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f[e].x, f[e].y);
     o[e] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  return r;
+  if constexpr (N == 4)
+    *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+  else
+    *reinterpret_cast<uint2*>(dst) = make_uint2(o[0], o[1]);
 }
 
-// position of token (b, n) on axis a
-__device__ __forceinline__ double rope_position(const RopeParams& p, int b, int n, int a) {
+// positions of token t on all axes: 64-bit integers (p.whole) or doubles
+__device__ __forceinline__ void rope_positions(const RopeParams& p, int t, long long* at) {
+  const int b = int(__umul64hi(uint64_t(t) << 1, p.n_magic)), n = t - b * p.N;
   if (p.pos) {
-    const long long at = b * p.pos_b + a * p.pos_a + n;
-    return p.pos_is_int ? double(static_cast<const int*>(p.pos)[at]) : double(static_cast<const float*>(p.pos)[at]);
+#pragma unroll
+    for (int a = 0; a < kRopeMaxAxes; ++a) {
+      if (a >= p.n_axes) break;
+      const long long i = b * p.pos_b + a * p.pos_a + n;
+      at[a] = p.pos_is_int ? static_cast<long long>(static_cast<const int*>(p.pos)[i])
+                           : __double_as_longlong(double(static_cast<const float*>(p.pos)[i]));
+    }
+    return;
   }
   unsigned long long i = static_cast<unsigned long long>(p.start) + n;
-  unsigned long long at = 0;
-  // the grid index holds below 2^32 for all but very long streams: then 32-bit divisions do
-  for (int x = p.n_axes - 1; x >= a; --x) {
-    const unsigned long long g = static_cast<unsigned long long>(p.grid[x]);
-    unsigned long long next;
-    if ((i | g) >> 32)
-      next = i / g;
-    else
-      next = uint32_t(i) / uint32_t(g);
-    at = i - next * g;
+#pragma unroll
+  for (int a = kRopeMaxAxes - 1; a >= 0; --a) {
+    if (a >= p.n_axes) continue;
+    // the grid index is below 2^32 for all but very long streams: then a 32-bit division does
+    const unsigned long long g = static_cast<unsigned long long>(p.grid[a]);
+    const unsigned long long next = ((i | g) >> 32) ? i / g : uint32_t(i) / uint32_t(g);
+    at[a] = static_cast<long long>(i - next * g);
     i = next;
   }
-  return double(at);
 }
 
-// Shared memory: [tpb][D/2] (cos, sin) | [tpb][heads] sums of squares | [tpb][2] scale of the row
-template <typename T, int D, bool HALVES, int U>
-__global__ void lite_rope_kernel(const __grid_constant__ RopeParams p) {
-  extern __shared__ float rope_smem[];
-  constexpr int C = D / 16;  // units (lanes) per head
-  const int heads = p.t[0].heads + p.t[1].heads;
-  float2* cs = reinterpret_cast<float2*>(rope_smem);
-  float* hsum = rope_smem + p.tpb * D;
-  float* rscale = hsum + p.tpb * heads;
-  const int first = int(blockIdx.x) * p.tpb;
-  const int n_tok = min(p.tpb, p.tokens - first);
-  const int total = n_tok * p.units;
-  using In = RopeIn<T>;
+constexpr int kRopeStages = 2;  // steps whose data are in shared memory or on their way
 
-  typename In::Raw lo[U], hi[U];
-  int tok[U], head[U], chunk[U], which[U];
+template <typename T, int U>
+struct RopeCfg {
+  static constexpr int E = 16 / sizeof(T);   // elements of a piece
+  static constexpr int RC = 16 / E;          // pieces of a unit
+  static constexpr int STEP = U * RC * 16;   // bytes of a thread's step
+};
+
+// The sizes of a block's shared memory: [stages][U * RC][threads] 16-byte pieces | frequencies [D/2],
+// axes [D/2] | two of each: positions [ahead][tpb][axes], (cos, sin) [ahead][tpb][D/2], sums of
+// squares [max(tpb * heads, warps)].
+struct RopeShape {
+  int units;   // units of a token: heads * D / 16
+  int tpb;     // tokens per block and step
+  int ahead;   // steps whose angles are computed at once
+  int threads;
+  __host__ __device__ int slots() const { return ahead * tpb; }
+  __host__ __device__ int sums(int heads) const { return (tpb * heads > 32 ? tpb * heads : 32); }
+  __host__ __device__ size_t bytes(int step, int D, int heads) const {
+    return size_t(kRopeStages) * step * threads + (D / 2) * 12 +
+           2 * (size_t(slots()) * (kRopeMaxAxes * 8 + D * 4) + size_t(sums(heads)) * 4);
+  }
+};
+
+// NORM: 0 none, 1 over the head, 2 over the token's heads. ONE: one token a step.
+template <typename T, int D, int U, int NORM, bool ONE>
+__global__ void __maxnreg__(128) lite_rope_kernel(const __grid_constant__ RopeParams p, const RopeShape sq,
+                                                         const RopeShape sk) {
+  extern __shared__ __align__(16) uint8_t rope_smem[];
+  constexpr int C = D / 16;  // units (lanes) per head
+  using R = RopeCfg<T, U>;
+  const bool keys = int(blockIdx.x) >= p.q_blocks;
+  const RopeShape sh = keys ? sk : sq;
+  const RopeTensor& x = p.t[keys];
+  const int block = keys ? int(blockIdx.x) - p.q_blocks : int(blockIdx.x);
+  const int n_blocks = keys ? int(gridDim.x) - p.q_blocks : p.q_blocks;
+  const int tpb = ONE ? 1 : sh.tpb, stride = n_blocks * tpb, heads = x.heads;
+  const int tid = threadIdx.x, threads = sh.threads, lane = tid & 31, warp = tid >> 5;
+  if (tid >= threads) return;  // (the other tensor's blocks are larger); barriers count `threads`
+  uint8_t* const pieces = rope_smem + tid * 16;
+  double* const turns = reinterpret_cast<double*>(rope_smem + kRopeStages * R::STEP * threads);
+  int* const axis = reinterpret_cast<int*>(turns + D / 2);
+  long long* const places = reinterpret_cast<long long*>(axis + D / 2);  // [2][slots][axes]
+  const int slots = sh.slots();
+  float* const tables = reinterpret_cast<float*>(places + 2 * slots * kRopeMaxAxes);
+  float* const sums = tables + 2 * slots * D;
+  const auto barrier = [&]() { asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory"); };
+
+  // This thread's units: token slot, head, chunk (the same for all of them where a step is one token).
+  int slot[U], head[U];
+  const int chunk = tid % C;
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const int flat = u * blockDim.x + threadIdx.x;
-    tok[u] = -1;
-    if (flat < total) {
-      const int tk = flat / p.units;
-      int rem = flat - tk * p.units;
-      const int w = rem >= p.units_q;
-      rem -= w ? p.units_q : 0;
-      tok[u] = tk;
-      which[u] = w;
-      head[u] = rem / C;
-      chunk[u] = rem % C;
-      const int b = (first + tk) / p.N, n = first + tk - b * p.N;
-      const RopeTensor& x = p.t[w];
-      const T* src = static_cast<const T*>(x.x) + b * x.xs[0] + n * x.xs[1] + head[u] * x.xs[2] + chunk[u] * 8;
-      lo[u] = In::load(src);
-      hi[u] = In::load(src + D / 2);
-    }
+    const int flat = u * threads + tid;
+    slot[u] = flat / sh.units;  // tpb (ONE: not 0) for a thread without a unit
+    head[u] = (flat - slot[u] * sh.units) / C;
   }
-
-  for (int i = threadIdx.x; i < n_tok * (D / 2); i += blockDim.x) {
-    const int tk = i / (D / 2), pr = i % (D / 2);
-    const int b = (first + tk) / p.N, n = first + tk - b * p.N;
-    const double turn = rope_position(p, b, n, p.axis[pr]) * p.turns[pr];
-    float s, c;
-    sincospif(2.0f * float(turn - rint(turn)), &s, &c);
-    cs[i] = make_float2(c, s);
-  }
-
-  float scale[U];
+  auto mine = [&](int u, int first) { return slot[u] < tpb && (ONE || first + slot[u] < p.tokens); };
+  // Where unit 0 of this thread's tokens starts: a cursor steps through the tokens of the block (ONE), an
+  // address is made anew only where a batch entry ends.
+  struct Cursor {
+    const uint8_t* at;
+    int n;  // token within its batch entry
+  };
+  auto place = [&](int t, const void* base, const long long* st, int h, int size) -> Cursor {
+    const int b = int(__umul64hi(uint64_t(t) << 1, p.n_magic)), n = t - b * p.N;
+    return Cursor{static_cast<const uint8_t*>(base) + (b * st[0] + n * st[1] + h * st[2] + chunk * R::E) * size, n};
+  };
+  auto advance = [&](Cursor& c, int t, long long step, const void* base, const long long* st, int size) {
+    c.n += stride;
+    c.at += step;
+    if (c.n >= p.N) c = place(t, base, st, head[0], size);
+  };
+  const long long in_step = stride * x.xs[1] * int(sizeof(T)), out_step = stride * x.ys[1] * 2;
+  // from one unit of the thread to its next one
+  const long long in_unit = (threads / C) * x.xs[2] * int(sizeof(T)), out_unit = (threads / C) * x.ys[2] * 2;
+  Cursor src_at = {nullptr, 0}, dst_at = {nullptr, 0};
+  auto load = [&](long long first, int stage) {
+    if (first < p.tokens) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) scale[u] = 1.f;
-  if (p.norm) {
+      for (int u = 0; u < U; ++u) {
+        if (!mine(u, int(first))) continue;
+        const uint8_t* src = ONE ? src_at.at + u * in_unit : place(int(first) + slot[u], x.x, x.xs, head[u], sizeof(T)).at;
+        uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(pieces)) + (stage * U + u) * R::RC * 16 * threads;
+#pragma unroll
+        for (int c = 0; c < R::RC; ++c) {
+          rope_copy16(dst, src + c * (D / R::RC) * sizeof(T));
+          dst += 16 * threads;
+        }
+      }
+      if (ONE && first + stride < p.tokens)
+        advance(src_at, int(first) + stride, in_step, x.x, x.xs, int(sizeof(T)));
+    }
+    rope_copies_commit();
+  };
+  // positions and angles of the steps from token `first` on, into table `which`
+  auto fill_places = [&](long long first, int which) {
+    for (int i = tid; i < slots; i += threads) {
+      const long long t = first + static_cast<long long>(i / tpb) * stride + i % tpb;
+      if (t < p.tokens) rope_positions(p, int(t), places + (which * slots + i) * kRopeMaxAxes);
+    }
+  };
+  auto fill_angles = [&](int which) {
+    for (int i = tid; i < slots * (D / 2); i += threads) {
+      const int s = which * slots + i / (D / 2), pr = i % (D / 2);
+      const long long at = places[s * kRopeMaxAxes + axis[pr]];
+      float half_turns;  // [-1, 1]
+      if (p.whole) {
+        const unsigned long long f = static_cast<unsigned long long>(at) * static_cast<unsigned long long>(__double_as_longlong(turns[pr]));
+        half_turns = float(int(f >> 32)) * 4.656612873077393e-10f;  // 2^-31
+      } else {
+        const double turn = __longlong_as_double(at) * turns[pr];
+        half_turns = 2.0f * float(turn - rint(turn));
+      }
+      const float phi = half_turns * 3.14159265358979f;
+      // entries of two (cos, sin) pairs, in the order in which the lanes of a head read them: entry e of
+      // piece j, lane c at (j * entries of a piece + e) * C + c
+      constexpr int PIECE = D / R::RC;
+      const int el = p.halves ? pr : 2 * pr, j = el / PIECE, rest = el % PIECE, c = rest / R::E;
+      const int e = p.halves ? rest % R::E / 2 : rest % R::E / 4, per = p.halves ? R::E / 2 : R::E / 4;
+      *reinterpret_cast<float2*>(tables + static_cast<size_t>(s) * D + ((j * per + e) * C + c) * 4 + (pr & 1) * 2) =
+          make_float2(__cosf(phi), __sinf(phi));
+    }
+  };
+
+  long long first = static_cast<long long>(block) * tpb;
+  if (ONE && first < p.tokens) {
+    src_at = place(int(first), x.x, x.xs, head[0], sizeof(T));
+    dst_at = place(int(first), x.y, x.ys, head[0], 2);
+  }
+#pragma unroll
+  for (int y = 0; y < kRopeStages - 1; ++y) load(first + static_cast<long long>(y) * stride, y);
+  // weights of the thread's units: they stay in registers
+  float4 w[NORM ? U : 1][4];
+  if constexpr (NORM != 0) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float ss = 0.f;
-      if (tok[u] >= 0) {
-        float a[8], b[8];
-        In::get(lo[u], a);
-        In::get(hi[u], b);
+      if (slot[u] >= tpb) continue;
+      const float* src = x.w + (NORM == 2 ? head[u] * D : 0) + chunk * R::E;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-      }
-#pragma unroll
-      for (int m = C / 2; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      if (p.norm == 1) {
-        scale[u] = rsqrtf(ss * (1.0f / D) + p.eps);
-      } else if (tok[u] >= 0 && chunk[u] == 0) {
-        hsum[tok[u] * heads + (which[u] ? p.t[0].heads : 0) + head[u]] = ss;
-      }
+      for (int e = 0; e < 4; ++e)
+        w[u][e] = __ldg(reinterpret_cast<const float4*>(src + 4 * e / R::E * (D / R::RC) + 4 * e % R::E));
     }
   }
-  __syncthreads();
-  if (p.norm == 2) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    for (int i = warp; i < n_tok * 2; i += warps) {
-      const int w = i & 1, h0 = w ? p.t[0].heads : 0, nh = p.t[w].heads;
-      const float* src = hsum + (i >> 1) * heads + h0;
-      float ss = 0.f;
-      for (int h = lane; h < nh; h += 32) ss += src[h];
-#pragma unroll
-      for (int m = 16; m; m >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-      if (lane == 0 && nh > 0) rscale[i] = rsqrtf(ss / (float(nh) * D) + p.eps);
-    }
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (tok[u] >= 0) scale[u] = rscale[tok[u] * 2 + which[u]];
+  for (int i = tid; i < D / 2; i += threads) {
+    turns[i] = p.turns[i];
+    axis[i] = p.axis[i];
   }
+  const long long table_span = static_cast<long long>(sh.ahead) * stride;
+  fill_places(first, 0);
+  fill_places(first + table_span, 1);
+  barrier();
+  fill_angles(0);
+  barrier();
 
+  int stage = 0, in_table = 0, table = 0;  // place of the step in its angle table, and which of the two
+  for (int step = 0; first < p.tokens; first += stride, ++step) {
+    // the stage loaded into was read by this thread in the step before
+    load(first + static_cast<long long>(kRopeStages - 1) * stride, stage == 0 ? kRopeStages - 1 : stage - 1);
+    rope_copies_left<kRopeStages - 1>();
+    float* hsum = sums + (step & 1) * sh.sums(heads);
+    uint4 raw[U][R::RC];
+    float ss[U];
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    if (tok[u] < 0) continue;
-    const RopeTensor& x = p.t[which[u]];
-    float a[8], b[8];
-    In::get(lo[u], a);
-    In::get(hi[u], b);
-    if (p.norm) {
-      const float* w = x.w + (p.norm == 2 ? head[u] * D : 0) + chunk[u] * 8;
-      const float4 w0 = __ldg(reinterpret_cast<const float4*>(w)), w1 = __ldg(reinterpret_cast<const float4*>(w) + 1);
-      const float4 w2 = __ldg(reinterpret_cast<const float4*>(w + D / 2)),
-                   w3 = __ldg(reinterpret_cast<const float4*>(w + D / 2) + 1);
-      const float wa[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-      const float wb[8] = {w2.x, w2.y, w2.z, w2.w, w3.x, w3.y, w3.z, w3.w};
+    for (int u = 0; u < U; ++u) {
+      const uint8_t* src = pieces + (stage * U + u) * R::RC * 16 * threads;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] *= scale[u] * wa[e];
-        b[e] *= scale[u] * wb[e];
+      for (int c = 0; c < R::RC; ++c) raw[u][c] = *reinterpret_cast<const uint4*>(src + c * 16 * threads);
+    }
+    constexpr int P2 = R::E / 2;  // element pairs of a piece
+    auto get = [&](int u, float2 (&v)[8]) {
+#pragma unroll
+      for (int c = 0; c < R::RC; ++c) rope_get(raw[u][c], static_cast<const T*>(nullptr), v + c * P2);
+    };
+    if constexpr (NORM != 0) {
+      float all = 0.f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float2 q = make_float2(0.f, 0.f);
+        if (mine(u, int(first))) {
+          float2 v[8];
+          get(u, v);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) q = __ffma2_rn(v[e], v[e], q);
+        }
+        ss[u] = q.x + q.y;
+        if (NORM == 1 || !ONE) {
+#pragma unroll
+          for (int m = C / 2; m; m >>= 1) ss[u] += __shfl_xor_sync(0xffffffffu, ss[u], m);
+          if (NORM == 2 && slot[u] < tpb && chunk == 0) hsum[slot[u] * heads + head[u]] = ss[u];
+        } else {
+          all += ss[u];
+        }
+      }
+      if (NORM == 2 && ONE) {
+#pragma unroll
+        for (int m = 16; m; m >>= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
+        if (lane == 0) hsum[warp] = all;
       }
     }
-    const float2* t = cs + tok[u] * (D / 2);
-    float ya[8], yb[8];
-    if (HALVES) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float2 r = t[chunk[u] * 8 + e];
-        ya[e] = a[e] * r.x - b[e] * r.y;
-        yb[e] = a[e] * r.y + b[e] * r.x;
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 r = t[chunk[u] * 4 + e], s = t[D / 4 + chunk[u] * 4 + e];
-        ya[2 * e] = a[2 * e] * r.x - a[2 * e + 1] * r.y;
-        ya[2 * e + 1] = a[2 * e] * r.y + a[2 * e + 1] * r.x;
-        yb[2 * e] = b[2 * e] * s.x - b[2 * e + 1] * s.y;
-        yb[2 * e + 1] = b[2 * e] * s.y + b[2 * e + 1] * s.x;
-      }
+    // new angles are seen from here on, and so are this step's sums
+    if (NORM == 2 || in_table == 0) barrier();
+    if (in_table == 0) {
+      // The other table's last readers have passed the barrier, and so have the writers of its positions.
+      // Positions for the table after it go where this table's were: read before the barrier.
+      fill_angles(table ^ 1);
+      fill_places(first + 2 * table_span, table);
     }
-    const int b0 = (first + tok[u]) / p.N, n = first + tok[u] - b0 * p.N;
-    __nv_bfloat16* dst = x.y + b0 * x.ys[0] + n * x.ys[1] + head[u] * x.ys[2] + chunk[u] * 8;
-    *reinterpret_cast<uint4*>(dst) = rope_pack(ya);
-    *reinterpret_cast<uint4*>(dst + D / 2) = rope_pack(yb);
+    float row = 0.f;
+    if constexpr (NORM == 2 && ONE) {
+      float sum = 0.f;
+      for (int i = 0; i < threads / 32; ++i) sum += hsum[i];
+      row = rsqrtf(sum / (float(heads) * D) + p.eps);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (!mine(u, int(first))) continue;
+      float2 v[8];
+      get(u, v);
+      if constexpr (NORM != 0) {
+        float scale;
+        if (NORM == 1) {
+          scale = rsqrtf(ss[u] * (1.0f / D) + p.eps);
+        } else if (ONE) {
+          scale = row;
+        } else {
+          // a token with few heads: its sums in index order
+          float sum = 0.f;
+          for (int h = 0; h < heads; ++h) sum += hsum[slot[u] * heads + h];
+          scale = rsqrtf(sum / (float(heads) * D) + p.eps);
+        }
+        const float2 s2 = make_float2(scale, scale);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = __fmul2_rn(__fmul2_rn(v[2 * e], s2), make_float2(w[u][e].x, w[u][e].y));
+          v[2 * e + 1] = __fmul2_rn(__fmul2_rn(v[2 * e + 1], s2), make_float2(w[u][e].z, w[u][e].w));
+        }
+      }
+      const float4* cs = reinterpret_cast<const float4*>(
+                             tables + static_cast<size_t>(table * slots + in_table * tpb + slot[u]) * D) + chunk;
+      float2 y[8];
+      if (p.halves) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // e / P2: piece, e % P2: entry
+          const float4 r = cs[e * C];
+          const float2 a = v[e], b = v[e + 4];
+          y[e] = make_float2(a.x * r.x - b.x * r.y, a.y * r.z - b.y * r.w);
+          y[e + 4] = make_float2(a.x * r.y + b.x * r.x, a.y * r.w + b.y * r.z);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 r = cs[e * C];
+          const float2 a = v[2 * e], b = v[2 * e + 1];
+          y[2 * e] = make_float2(a.x * r.x - a.y * r.y, a.x * r.y + a.y * r.x);
+          y[2 * e + 1] = make_float2(b.x * r.z - b.y * r.w, b.x * r.w + b.y * r.z);
+        }
+      }
+      uint8_t* dst = const_cast<uint8_t*>(ONE ? dst_at.at + u * out_unit
+                                              : place(int(first) + slot[u], x.y, x.ys, head[u], 2).at);
+#pragma unroll
+      for (int c = 0; c < R::RC; ++c) rope_put<P2>(dst + c * (D / R::RC) * 2, y + c * P2);
+    }
+    if (ONE && first + stride < p.tokens) advance(dst_at, int(first) + stride, out_step, x.y, x.ys, 2);
+    stage = stage + 1 == kRopeStages ? 0 : stage + 1;
+    if (++in_table == sh.ahead) {
+      in_table = 0;
+      table ^= 1;
+    }
   }
+  rope_copies_left<0>();
 }
 
 }  // namespace lite

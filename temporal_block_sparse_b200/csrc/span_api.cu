@@ -23,6 +23,8 @@ constexpr int kMaxDevices = 64;
 
 cudaStream_t as_stream(lite_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 // ------------------------------------------------------------------------------------- rotation
 
 // Strides (batch, token, head) of a [B, N, heads, d] tensor: non-negative, multiples of `unit`
@@ -34,24 +36,74 @@ bool rope_strides_ok(const int64_t* s, int B, int N, int heads, int unit) {
   return true;
 }
 
-template <typename T, int D, bool HALVES>
-int launch_rope(const lite::RopeParams& p0, cudaStream_t stream) {
-  lite::RopeParams p = p0;
-  constexpr int U = 2;  // units of a thread
-  // tokens per block: as many as fit 512 units; a token with more units has a block of its own
-  p.tpb = std::max(1, 512 / p.units);
-  const int threads = (p.tpb * p.units + U * 32 - 1) / (U * 32) * 32;
-  const long long blocks = (static_cast<long long>(p.tokens) + p.tpb - 1) / p.tpb;
-  const int heads = p.t[0].heads + p.t[1].heads;
-  const size_t smem = size_t(p.tpb) * (D + heads + 2) * sizeof(float);
-  lite::lite_rope_kernel<T, D, HALVES, U><<<unsigned(blocks), threads, smem, stream>>>(p);
+// Turns per position of angular frequency f; for whole positions its fractional part as a 64-bit
+// fraction (in the bits of the double).
+double turns_of(double f, bool whole) {
+  const long double t = static_cast<long double>(f) / 6.283185307179586476925286766559L;
+  if (!whole) return static_cast<double>(t);
+  const long double part = t - floorl(t);
+  const uint64_t bits = part >= 1.0L ? 0 : static_cast<uint64_t>(part * 18446744073709551616.0L);
+  double out;
+  std::memcpy(&out, &bits, sizeof(out));
+  return out;
+}
+
+lite::RopeShape rope_shape(int heads, int d, int U) {
+  lite::RopeShape sh;
+  sh.units = heads * (d / 16);
+  // as many tokens as fit 256 units; a token with more units has a block of its own
+  sh.tpb = std::max(1, 256 / std::max(sh.units, 1));
+  sh.threads = (sh.tpb * sh.units + U * 32 - 1) / (U * 32) * 32;
+  sh.ahead = std::min(8, std::max(1, sh.threads / (sh.tpb * (d / 2))));
+  return sh;
+}
+
+template <typename T, int D, int U, int NORM, bool ONE>
+int launch_rope(lite::RopeParams p, const DeviceContext& dc, cudaStream_t stream) {
+  const auto kernel = lite::lite_rope_kernel<T, D, U, NORM, ONE>;
+  const lite::RopeShape sq = rope_shape(p.t[0].heads, D, U), sk = rope_shape(std::max(p.t[1].heads, 1), D, U);
+  const bool keys = p.t[1].heads > 0;
+  const int threads = keys ? std::max(sq.threads, sk.threads) : sq.threads;
+  size_t smem = sq.bytes(lite::RopeCfg<T, U>::STEP, D, p.t[0].heads);
+  if (keys) smem = std::max(smem, sk.bytes(lite::RopeCfg<T, U>::STEP, D, p.t[1].heads));
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
+    return LITE_ERR_CUDA;
+  const int64_t need_q = ceil_div(p.tokens, sq.tpb), need_k = keys ? ceil_div(p.tokens, sk.tpb) : 0;
+  int64_t q_blocks = need_q, k_blocks = need_k;
+  if (need_q + need_k > dc.sms) {
+    // persistent: every resident block, shared out by the tensors' work
+    int per_sm = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess)
+      return LITE_ERR_CUDA;
+    const int64_t all = std::max<int64_t>(2, int64_t(dc.sms) * std::max(per_sm, 1));
+    if (need_q + need_k > all) {
+      const double part = keys ? double(need_q * sq.threads) / double(need_q * sq.threads + need_k * sk.threads) : 1.0;
+      q_blocks = std::min(need_q, std::max<int64_t>(1, keys ? std::min<int64_t>(all - 1, int64_t(part * all + 0.5)) : all));
+      k_blocks = std::min(need_k, all - q_blocks);
+    }
+  }
+  p.q_blocks = int(q_blocks);
+  kernel<<<unsigned(q_blocks + k_blocks), threads, smem, stream>>>(p, sq, sk);
   return cudaGetLastError() == cudaSuccess ? LITE_OK : LITE_ERR_CUDA;
 }
 
+template <typename T, int D, int NORM>
+int launch_rope_u(const lite::RopeParams& p, const DeviceContext& dc, cudaStream_t stream) {
+  // two units a thread: a token of up to 1024 units fits a block
+  const bool one = rope_shape(p.t[0].heads, D, 2).tpb == 1 &&
+                   (p.t[1].heads == 0 || rope_shape(p.t[1].heads, D, 2).tpb == 1);
+  return one ? launch_rope<T, D, 2, NORM, true>(p, dc, stream) : launch_rope<T, D, 2, NORM, false>(p, dc, stream);
+}
+
 template <typename T>
-int launch_rope_d(const lite::RopeParams& p, int d, int pairing, cudaStream_t stream) {
-  if (d == 64) return pairing ? launch_rope<T, 64, true>(p, stream) : launch_rope<T, 64, false>(p, stream);
-  return pairing ? launch_rope<T, 128, true>(p, stream) : launch_rope<T, 128, false>(p, stream);
+int launch_rope_d(const lite::RopeParams& p, const lite_rope_args& a, const DeviceContext& dc, cudaStream_t stream) {
+  if (a.d == 64) {
+    if (a.norm == 0) return launch_rope_u<T, 64, 0>(p, dc, stream);
+    return a.norm == 1 ? launch_rope_u<T, 64, 1>(p, dc, stream) : launch_rope_u<T, 64, 2>(p, dc, stream);
+  }
+  if (a.norm == 0) return launch_rope_u<T, 128, 0>(p, dc, stream);
+  return a.norm == 1 ? launch_rope_u<T, 128, 1>(p, dc, stream) : launch_rope_u<T, 128, 2>(p, dc, stream);
 }
 
 // ------------------------------------------------------------------------------------ attention
@@ -130,8 +182,6 @@ int check_attention(const lite_span_args& a, bool prefix) {
   return LITE_OK;
 }
 
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
 // One pass over query tiles (see SpanPass): `units` key heads (times batch entries), each with
 // `tokens` tokens against `tiles` key tiles.
 struct PassPlan {
@@ -163,8 +213,8 @@ PassPlan make_pass(int64_t units, int64_t tokens, int G, int64_t tiles) {
 // Microseconds that one CTA takes for an item of t key tiles: its start and end, and each tile, as
 // measured on a B200 with all CTAs busy (a d = 64 tile has half the keys and shares its SM).
 double item_us(const PassPlan& ps, int d, int64_t t) {
-  const double tile = ps.F == 4 ? (d == 64 ? 0.75 : 1.4) : ps.alt ? (d == 64 ? 0.9 : 1.6) : (d == 64 ? 1.7 : 2.5);
-  return 3.0 + tile * double(t);
+  const double tile = ps.F == 4 ? (d == 64 ? 1.0 : 1.35) : ps.alt ? (d == 64 ? 0.9 : 1.4) : (d == 64 ? 1.75 : 2.4);
+  return 4.0 + tile * double(t);
 }
 
 // Time of both passes' items on `slots` CTAs: whole waves where all items are alike, else the
@@ -383,11 +433,22 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   if (!st && pl.parts) {
     const int64_t threads = int64_t(a.B) * a.Nq * a.H * (a.d / 4);
     const unsigned blocks = unsigned(ceil_div(threads, 256));
-    if (a.d == 64)
-      lite::lite_span_combine_kernel<64><<<blocks, 256, 0, stream>>>(p);
-    else
-      lite::lite_span_combine_kernel<128><<<blocks, 256, 0, stream>>>(p);
-    if (cudaGetLastError() != cudaSuccess) st = LITE_ERR_CUDA;
+    // Launched while the parts are still being written (it waits for them itself), so that its
+    // start-up is hidden.
+    cudaLaunchConfig_t cfg;
+    std::memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    std::memset(&attr, 0, sizeof(attr));
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, a.d == 64 ? lite::lite_span_combine_kernel<64> : lite::lite_span_combine_kernel<128>,
+                           p) != cudaSuccess)
+      st = LITE_ERR_CUDA;
   }
   if (ws && cudaFreeAsync(ws, stream) != cudaSuccess && !st) st = LITE_ERR_CUDA;
   return st;
@@ -433,8 +494,8 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream) {
   if (keys && (!rope_strides_ok(a.k_stride, a.B, a.N, a.Hk, unit) || !rope_strides_ok(a.k_out_stride, a.B, a.N, a.Hk, 8)))
     return LITE_ERR_UNSUPPORTED;
   // a block holds a whole token, two units of 16 elements a thread
-  const int64_t units = (int64_t(a.H) + (keys ? a.Hk : 0)) * (a.d / 16);
-  if (units > 2048 || int64_t(a.B) * a.N > INT_MAX - 1024) return LITE_ERR_UNSUPPORTED;
+  if (int64_t(a.H) * a.d > 16384 || (keys && int64_t(a.Hk) * a.d > 16384) || int64_t(a.B) * a.N > (1 << 30))
+    return LITE_ERR_UNSUPPORTED;
   DeviceContext dc;
   if (lite_host::device_context(false, &dc) != LITE_OK) return LITE_ERR_CUDA;
   lite::RopeParams p;
@@ -454,9 +515,8 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream) {
   if (keys) fill(p.t[1], a.k, a.k_out, a.k_weight, a.k_stride, a.k_out_stride, a.Hk);
   p.tokens = a.B * a.N;
   p.N = a.N;
-  p.units = int(units);
-  p.units_q = a.H * (a.d / 16);
-  p.norm = a.norm;
+  p.n_magic = (uint64_t(1) << 63) / uint64_t(a.N) + 1;
+  p.halves = a.pairing;
   p.eps = a.eps;
   p.n_axes = a.n_axes;
   p.start = a.start;
@@ -466,14 +526,15 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream) {
   p.pos_is_int = a.pos_dtype == LITE_INT32;
   p.pos_b = a.pos_batch_stride;
   p.pos_a = a.pos_axis_stride;
+  p.whole = !a.pos || p.pos_is_int;
   for (int x = 0; x < a.d / 2; ++x) {
-    p.turns[x] = a.freq[x] / 6.283185307179586476925;
+    p.turns[x] = turns_of(a.freq[x], p.whole);
     p.axis[x] = uint8_t(a.axis[x]);
   }
   switch (a.dtype) {
-    case LITE_BF16: return launch_rope_d<__nv_bfloat16>(p, a.d, a.pairing, as_stream(stream));
-    case LITE_FP16: return launch_rope_d<__half>(p, a.d, a.pairing, as_stream(stream));
-    default: return launch_rope_d<float>(p, a.d, a.pairing, as_stream(stream));
+    case LITE_BF16: return launch_rope_d<__nv_bfloat16>(p, a, dc, as_stream(stream));
+    case LITE_FP16: return launch_rope_d<__half>(p, a, dc, as_stream(stream));
+    default: return launch_rope_d<float>(p, a, dc, as_stream(stream));
   }
 }
 

@@ -857,13 +857,14 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
 }
 
 // Joins the parts of every output row: M = max m_i, o = sum 2^(m_i - M) O_i / L, L = sum 2^(m_i - M) l_i.
-// One group of D/4 lanes per row. Bound by the parts' bytes; they were written just before and are in L2.
+// One group of D/4 lanes per row, which reads the maxima of its parts at once and then the parts four at
+// a time. Bound by latency: the parts were written just before and are in L2.
 template <int D>
 __global__ void __launch_bounds__(256) lite_span_combine_kernel(const SpanParams p) {
   constexpr int L = D / 4;  // lanes of a row
   const long long row = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / L;
   const int lane = threadIdx.x % L;
-  if (row >= static_cast<long long>(p.B) * p.Nq * p.H) return;
+  if (row >= static_cast<long long>(p.B) * p.Nq * p.H) return;  // (whole groups of lanes)
   const int h = int(row % p.H);
   const long long bn = row / p.H;
   const int b = int(bn / p.Nq), n = int(bn - static_cast<long long>(b) * p.Nq);
@@ -885,26 +886,51 @@ __global__ void __launch_bounds__(256) lite_span_combine_kernel(const SpanParams
     count[k] = ps.alt ? ps.splits * ps.per_item : ps.splits;
     step[k] = (ps.alt ? 1 : ps.per_item) * SpanPart<D>::FLOATS;
   }
-  float m = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
-    for (int i = 0; i < count[k]; ++i) m = fmaxf(m, part[k][i * step[k] + 128 * D + at[k]]);
+  const int total = count[0] + count[1];
+  const auto part_at = [&](int i) -> const float* {
+    return i < count[0] ? part[0] + i * step[0] + at[0] * D : part[1] + (i - count[0]) * step[1] + at[1] * D;
+  };
+  // the scratch is the kernel's before this one in the stream
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float m = -INFINITY, tot = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float tot = 0.f;
+  const unsigned lanes = L == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);  // the row's lanes of the warp
+  for (int base = 0; base < total; base += L) {
+    // lane i brings maximum and sum of part base + i, then all lanes take the parts in order
+    float mi = -INFINITY, li = 0.f;
+    if (base + lane < total) {
+      const int i = base + lane;
+      const float* q = i < count[0] ? part[0] + i * step[0] + 128 * D + at[0]
+                                    : part[1] + (i - count[0]) * step[1] + 128 * D + at[1];
+      mi = q[0];
+      li = q[128];
+    }
+    float top = mi;
 #pragma unroll
-  for (int k = 0; k < 2; ++k)
-    for (int i = 0; i < count[k]; ++i) {
-      const float* q = part[k] + i * step[k];
-      const float mi = q[128 * D + at[k]], li = q[128 * D + 128 + at[k]];
-      if (li == 0.f) continue;  // the part saw no key
-      const float w = m == -INFINITY ? 1.f : exp2f(mi - m);
-      const float4 x = *reinterpret_cast<const float4*>(q + at[k] * D + lane * 4);
+    for (int x = L / 2; x; x >>= 1) top = fmaxf(top, __shfl_xor_sync(lanes, top, x));
+    top = fmaxf(top, m);
+    const float keep = m == top ? 1.f : exp2f(m - top);  // (m may be -inf: nothing is kept then)
+    // a part that saw no key weighs nothing; one without a maximum but with a NaN sum passes it on
+    const float wi = li == 0.f ? 0.f : (top == -INFINITY ? 1.f : exp2f(mi - top));
+    m = top;
+    acc.x *= keep;
+    acc.y *= keep;
+    acc.z *= keep;
+    acc.w *= keep;
+    tot *= keep;
+    const int n = min(L, total - base);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float w = __shfl_sync(lanes, wi, i, L), lw = __shfl_sync(lanes, li, i, L);
+      if (lw == 0.f) continue;
+      const float4 x = *reinterpret_cast<const float4*>(part_at(base + i) + lane * 4);
       acc.x = fmaf(w, x.x, acc.x);
       acc.y = fmaf(w, x.y, acc.y);
       acc.z = fmaf(w, x.z, acc.z);
       acc.w = fmaf(w, x.w, acc.w);
-      tot = fmaf(w, li, tot);
+      tot = fmaf(w, lw, tot);
     }
+  }
   const float inv = tot == 0.f ? 0.f : 1.f / tot;
   const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * inv, acc.y * inv), z = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
   uint2 out;

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -52,9 +53,9 @@ SIGNATURES = {
     "lite_mask_to_ranges": ([_P, _P, _P, _I, _I, _I, _I, _P], _I),
     "lite_set_cta_timing": ([_P, _I], _I),
     "lite_scratch_pool_bytes": ([ctypes.POINTER(ctypes.c_longlong)], _I),
-    "lite_qk_rope": ([_P, _P], _I),
-    "lite_attn_span": ([_P, _P], _I),
-    "lite_attn_prefix": ([_P, _P], _I),
+    "lite_qk_rope": ([ctypes.c_char_p, _P], _I),
+    "lite_attn_span": ([ctypes.c_char_p, _P], _I),
+    "lite_attn_prefix": ([ctypes.c_char_p, _P], _I),
     "lite_attn_fwd_list": ([_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _F, _F, _P], _I),
 }
 MAX_MERGE_PARTS = 8
@@ -438,63 +439,47 @@ def lite_set_cta_timing(buf: Optional[torch.Tensor]):
 
 LITE_BF16, LITE_FP16, LITE_FP32, LITE_INT32 = 0, 1, 2, 3
 _I32, _I64 = ctypes.c_int32, ctypes.c_int64
-_S3 = _I64 * 3
+
+# lite_rope_args and lite_span_args of include/lite_attn.h, field by field (packed in one call: these
+# operators are also used on a few tokens, where the time of the call itself counts)
+_ROPE_ARGS = struct.Struct("=4Q12q5Q2qQq10if4x")
+_SPAN_ARGS = struct.Struct("=12Q15q9i2f4x")
 
 
-class _RopeArgs(ctypes.Structure):
-    """lite_rope_args of include/lite_attn.h."""
-
-    _fields_ = [(n, _P) for n in ("q", "k", "q_out", "k_out")]
-    _fields_ += [(n, _S3) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
-    _fields_ += [(n, _P) for n in ("q_weight", "k_weight", "freq", "axis", "pos")]
-    _fields_ += [("pos_batch_stride", _I64), ("pos_axis_stride", _I64), ("grid", _P), ("start", _I64)]
-    _fields_ += [(n, _I32) for n in ("dtype", "pos_dtype", "norm", "pairing", "n_axes", "B", "N", "H", "Hk", "d")]
-    _fields_ += [("eps", _F)]
-
-
-class _SpanArgs(ctypes.Structure):
-    """lite_span_args of include/lite_attn.h."""
-
-    _fields_ = [(n, _P) for n in ("q", "k", "v", "k_prefix", "v_prefix", "o", "lse", "spans", "slopes", "q_pos",
-                                  "k_pos", "prefix_pos")]
-    _fields_ += [(n, _S3) for n in ("q_stride", "k_stride", "v_stride", "k_prefix_stride", "v_prefix_stride")]
-    _fields_ += [(n, _I32) for n in ("B", "Nq", "Nk", "Np", "H", "Hk", "d", "span_batches", "pos_batches")]
-    _fields_ += [("scale", _F), ("cap", _F)]
-
-
-def _call_on(fn: str, args, device: torch.device, stream):
-    """Calls library function `fn` on `stream` (default: the current stream of `device`) with `device` current."""
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if device.index == torch.cuda.current_device():
-        st = getattr(load(), fn)(ctypes.addressof(args), stream.cuda_stream)
+def _call_on(fn: str, args: bytes, index: int, stream):
+    """Calls library function `fn` on `stream` (default: the current stream of device `index`) with that device current."""
+    handle = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    call = getattr(_lib or load(), fn)
+    if index == torch._C._cuda_getDevice():
+        st = call(args, handle)
     else:
-        with torch.cuda.device(device):
-            st = getattr(load(), fn)(ctypes.addressof(args), stream.cuda_stream)
+        with torch.cuda.device(index):
+            st = call(args, handle)
     if st != LITE_OK:
         raise LiteAttnError(fn, st)
 
 
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """An output made for work on `stream`: its memory is not handed out again before that work is done."""
+def _new(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """An output on the device of `like`, made for work on `stream`: its memory is not handed out again
+    before that work is done."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _check_stream(stream, device):
-    if stream is not None and stream.device != device:
+def _check_stream(stream, index: int):
+    if stream is not None and stream.device.index != index:
         raise ValueError("stream must be on the device of q")
 
 
-def _check_rows(name: str, t: torch.Tensor, dtypes, unit: int, device, batch_zero: bool = False):
-    """A CUDA tensor [B, N, heads, d] of one of `dtypes` on `device` whose head dimension is
+def _check_rows(name: str, t: torch.Tensor, dtypes, unit: int, index: int, batch_zero: bool = False):
+    """A CUDA tensor [B, N, heads, d] of one of `dtypes` on device `index` whose head dimension is
     contiguous and whose other strides are multiples of `unit` elements (16 bytes)."""
     if t.dim() != 4 or not t.is_cuda or t.dtype not in dtypes:
         raise ValueError(f"{name} must be a 4-D CUDA tensor [B, N, heads, d] of type "
                          f"{' or '.join(str(x)[6:] for x in dtypes)}")
-    if t.device != device:
+    if t.get_device() != index:
         raise ValueError(f"{name} must be on the device of q")
     size, stride = t.shape, t.stride()
     if size[3] > 1 and stride[3] != 1:
@@ -506,9 +491,26 @@ def _check_rows(name: str, t: torch.Tensor, dtypes, unit: int, device, batch_zer
         raise ValueError(f"{name} must be 16-byte aligned")
 
 
-def _strides(t: torch.Tensor):
-    st = t.stride()
-    return _S3(st[0], st[1], st[2])
+def _rows(name: str, t: torch.Tensor, dtypes, unit: int, index: int, batch_zero: bool = False):
+    """(shape, strides, address) of a tensor that passes _check_rows."""
+    size, st, at = t.shape, t.stride(), t.data_ptr()
+    # what nearly every call passes; anything else is looked at dimension by dimension
+    if not (len(size) == 4 and t.dtype in dtypes and t.get_device() == index >= 0 and st[3] == 1
+            and st[0] > 0 and st[1] > 0 and st[2] > 0 and not ((st[0] | st[1] | st[2]) & (unit - 1)) and not at & 15):
+        _check_rows(name, t, dtypes, unit, index, batch_zero)
+    return size, st, at
+
+
+_BF16 = (torch.bfloat16,)
+
+
+def _rows3(name: str, t: torch.Tensor, index: int):
+    """_rows for a bf16 tensor [N, heads, d]: as if it had a batch dimension of one entry."""
+    size, st, at = t.shape, t.stride(), t.data_ptr()
+    if not (t.dtype is torch.bfloat16 and t.get_device() == index >= 0 and st[2] == 1 and st[0] > 0 and st[1] > 0
+            and not ((st[0] | st[1]) & 7) and not at & 15):
+        _check_rows(name, t[None], _BF16, 8, index)
+    return (1, *size), (0, *st), at
 
 
 class RopePlan:
@@ -545,15 +547,18 @@ class RopePlan:
         self.axis, self.freq = axis, freq
         self._axis = (_I32 * len(axis))(*axis)
         self._freq = (ctypes.c_double * len(freq))(*freq)
+        self._axis_at, self._freq_at = ctypes.addressof(self._axis), ctypes.addressof(self._freq)
+        self._halves = int(pairing == "half")
 
 
 _ROPE_TYPES = {torch.bfloat16: LITE_BF16, torch.float16: LITE_FP16, torch.float32: LITE_FP32}
 
 
-def _check_weight(name: str, w: torch.Tensor, sizes, device):
-    if w.dtype != torch.float32 or not w.is_contiguous() or w.device != device or w.dim() != 1 or w.numel() not in sizes:
-        raise ValueError(f"{name} must be a contiguous fp32 tensor of {' or '.join(str(x) for x in sizes)} elements "
-                         "on the device of q")
+def _check_weight(name: str, w: torch.Tensor, sizes, index: int):
+    if (w.dtype != torch.float32 or not w.is_contiguous() or w.get_device() != index or w.dim() != 1
+            or w.numel() not in sizes or w.data_ptr() % 16):
+        raise ValueError(f"{name} must be a contiguous, 16-byte aligned fp32 tensor of "
+                         f"{' or '.join(str(x) for x in sizes)} elements on the device of q")
 
 
 def lite_qk_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan, grid=None, start: int = 0,
@@ -569,151 +574,151 @@ def lite_qk_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan, gri
     itself, weights of heads * d elements norm the token's whole row. q_out / k_out may be given (a
     slice of a key cache, or q / k themselves for bf16 in place).
     """
-    dev = q.device
-    if q.dtype not in _ROPE_TYPES:
+    dev = q.get_device()
+    dtype = q.dtype
+    if dtype not in _ROPE_TYPES:
         raise ValueError("q must be bf16, fp16 or fp32")
-    unit = 4 if q.dtype == torch.float32 else 8
-    _check_rows("q", q, (q.dtype,), unit, dev)
-    _check_stream(stream, dev)
-    B, N, H, d = q.shape
+    types, unit = (dtype,), 4 if dtype == torch.float32 else 8
+    (B, N, H, d), qs, q_at = _rows("q", q, types, unit, dev)
+    if stream is not None:
+        _check_stream(stream, dev)
     if plan.d != d:
         raise ValueError(f"the plan is for head dimension {plan.d}, q has {d}")
-    a = _RopeArgs()
-    Hk = 0
+    Hk, ks, k_at = 0, (0, 0, 0, 0), 0
     if k is not None:
-        _check_rows("k", k, (q.dtype,), unit, dev)
-        Hk = k.shape[2]
-        if k.shape[:2] != q.shape[:2] or k.shape[3] != d:
+        k_size, ks, k_at = _rows("k", k, types, unit, dev)
+        Hk = k_size[2]
+        if k_size != (B, N, Hk, d):
             raise ValueError("q [B, N, H, d] and k [B, N, Hk, d] must agree in B, N and d")
     if (pos is None) == (grid is None):
         raise ValueError("give either grid or pos")
     axes = len(plan.dims)
+    cells, pos_at, pos_type, pos_b, pos_a = 0, 0, 0, 0, 0
     if pos is None:
-        grid = [int(x) for x in grid]
-        if len(grid) != axes or any(not 0 < x < 1 << 63 for x in grid):
+        grid, start = tuple(map(int, grid)), int(start)
+        if len(grid) != axes or min(grid) <= 0 or max(grid) >= 1 << 63:
             raise ValueError(f"grid: {axes} positive sizes")
-        if not 0 <= start <= math.prod(grid) - N:
+        if not 0 <= start <= math.prod(grid) - N or start >= 1 << 62:
             raise ValueError("tokens start .. start + N - 1 must lie in the grid")
-        cells = (_I64 * axes)(*grid)
-        a.grid, a.start = ctypes.addressof(cells), int(start)
+        sizes = (_I64 * axes)(*grid)
+        cells = ctypes.addressof(sizes)
     else:
         if start:
             raise ValueError("start belongs to grid")
-        if (pos.dtype not in (torch.float32, torch.int32) or pos.device != dev or not pos.is_contiguous()
+        if (pos.dtype not in (torch.float32, torch.int32) or pos.get_device() != dev or not pos.is_contiguous()
                 or tuple(pos.shape) not in ((axes, N), (1, axes, N), (B, axes, N))):
             raise ValueError(f"pos must be a contiguous fp32 or int32 tensor [{axes}, N] or [B, {axes}, N] on the device of q")
-        a.pos, a.pos_dtype = pos.data_ptr(), LITE_FP32 if pos.dtype == torch.float32 else LITE_INT32
-        a.pos_axis_stride, a.pos_batch_stride = N, axes * N if pos.dim() == 3 and pos.shape[0] > 1 else 0
+        pos_at, pos_type = pos.data_ptr(), LITE_FP32 if pos.dtype == torch.float32 else LITE_INT32
+        pos_a, pos_b = N, axes * N if pos.dim() == 3 and pos.shape[0] > 1 else 0
     if k is not None and (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
     if k is None and (k_weight is not None or k_out is not None):
         raise ValueError("k_weight and k_out need k")
+    norm, eps, qw_at, kw_at = 0, float(eps), 0, 0
     if q_weight is not None:
         _check_weight("q_weight", q_weight, (d, H * d), dev)
         rows = q_weight.numel() != d
         if k is not None:
             _check_weight("k_weight", k_weight, (d, Hk * d), dev)
-            if H > 1 and Hk > 1 and rows != (k_weight.numel() != d):
-                raise ValueError("q_weight and k_weight must both be per head or both per row")
-            # with one head the two norms are the same: the other tensor decides
+            # (with one head the two norms are the same: the other tensor decides)
             rows = rows or k_weight.numel() != d
             if rows and (q_weight.numel() != H * d or k_weight.numel() != Hk * d):
                 raise ValueError("q_weight and k_weight must both be per head or both per row")
-        a.norm, a.eps = 2 if rows else 1, float(eps)
-        if not (a.eps >= 0.0 and math.isfinite(a.eps)):
+            kw_at = k_weight.data_ptr()
+        norm, qw_at = 2 if rows else 1, q_weight.data_ptr()
+        if not 0.0 <= eps < math.inf:
             raise ValueError("eps must be a non-negative number")
-        a.q_weight = q_weight.data_ptr()
-        a.k_weight = None if k is None else k_weight.data_ptr()
     if q_out is None:
-        q_out = _new((B, N, H, d), torch.bfloat16, dev, stream)
+        q_out = _new(q, (B, N, H, d), torch.bfloat16, stream)
+        qos, qo_at = (N * H * d, H * d, d), q_out.data_ptr()
     else:
-        _check_rows("q_out", q_out, (torch.bfloat16,), 8, dev)
-        if q_out.shape != q.shape:
+        qo_size, qos, qo_at = _rows("q_out", q_out, _BF16, 8, dev)
+        if qo_size != q.shape:
             raise ValueError("q_out must have q's shape")
-    a.q, a.q_out, a.q_stride, a.q_out_stride = q.data_ptr(), q_out.data_ptr(), _strides(q), _strides(q_out)
+    kos, ko_at = ks, 0
     if k is not None:
         if k_out is None:
-            k_out = _new((B, N, Hk, d), torch.bfloat16, dev, stream)
+            k_out = _new(q, (B, N, Hk, d), torch.bfloat16, stream)
+            kos, ko_at = (N * Hk * d, Hk * d, d), k_out.data_ptr()
         else:
-            _check_rows("k_out", k_out, (torch.bfloat16,), 8, dev)
-            if k_out.shape != k.shape:
+            ko_size, kos, ko_at = _rows("k_out", k_out, _BF16, 8, dev)
+            if ko_size != k_size:
                 raise ValueError("k_out must have k's shape")
-        a.k, a.k_out, a.k_stride, a.k_out_stride = k.data_ptr(), k_out.data_ptr(), _strides(k), _strides(k_out)
-    a.freq, a.axis, a.n_axes = ctypes.addressof(plan._freq), ctypes.addressof(plan._axis), axes
-    a.dtype, a.pairing = _ROPE_TYPES[q.dtype], int(plan.pairing == "half")
-    a.B, a.N, a.H, a.Hk, a.d = B, N, H, Hk, d
-    _call_on("lite_qk_rope", a, dev, stream)
+    args = _ROPE_ARGS.pack(q_at, k_at, qo_at, ko_at, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], qos[0], qos[1], qos[2],
+                           kos[0], kos[1], kos[2], qw_at, kw_at, plan._freq_at, plan._axis_at, pos_at, pos_b, pos_a,
+                           cells, start, _ROPE_TYPES[dtype], pos_type, norm, plan._halves, axes, B, N, H, Hk, d, eps)
+    _call_on("lite_qk_rope", args, dev, stream)
     return q_out, k_out
 
 
 def _span_call(fn: str, q, k, v, k_prefix, v_prefix, spans, scale, cap, slopes, q_pos, k_pos, prefix_pos, o, lse,
                return_lse, stream):
-    dev = q.device
-    bf16 = (torch.bfloat16,)
-    _check_rows("q", q, bf16, 8, dev, batch_zero=True)
-    _check_rows("k", k, bf16, 8, dev, batch_zero=True)
-    _check_rows("v", v, bf16, 8, dev, batch_zero=True)
-    _check_stream(stream, dev)
-    B, Nq, H, d = q.shape
-    Nk, Hk = k.shape[1], k.shape[2]
-    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != d:
+    dev = q.get_device()
+    (B, Nq, H, d), qs, q_at = _rows("q", q, _BF16, 8, dev, True)
+    k_size, ks, k_at = _rows("k", k, _BF16, 8, dev, True)
+    v_size, vs, v_at = _rows("v", v, _BF16, 8, dev, True)
+    if stream is not None:
+        _check_stream(stream, dev)
+    _, Nk, Hk, _ = k_size
+    if k_size != v_size or k_size[0] != B or k_size[3] != d:
         raise ValueError("q [B, Nq, H, d] and k, v [B, Nk, Hk, d] must agree in B and d, k and v in shape")
     if Hk == 0 or H % Hk:
         raise ValueError("the heads of k must divide the heads of q")
-    a = _SpanArgs()
-    a.q, a.k, a.v = q.data_ptr(), k.data_ptr(), v.data_ptr()
-    a.q_stride, a.k_stride, a.v_stride = _strides(q), _strides(k), _strides(v)
-    Np = 0
+    Np, kps, vps, kp_at, vp_at = 0, (0, 0, 0, 0), (0, 0, 0, 0), 0, 0
     if k_prefix is not None:
         if k_prefix.dim() == 3 and v_prefix.dim() == 3:
-            k_prefix, v_prefix = k_prefix[None], v_prefix[None]
-        _check_rows("k_prefix", k_prefix, bf16, 8, dev)
-        _check_rows("v_prefix", v_prefix, bf16, 8, dev)
-        Np = k_prefix.shape[1]
-        if k_prefix.shape != v_prefix.shape or tuple(k_prefix.shape) != (1, Np, Hk, d):
+            kp_size, kps, kp_at = _rows3("k_prefix", k_prefix, dev)
+            vp_size, vps, vp_at = _rows3("v_prefix", v_prefix, dev)
+        else:
+            kp_size, kps, kp_at = _rows("k_prefix", k_prefix, _BF16, 8, dev)
+            vp_size, vps, vp_at = _rows("v_prefix", v_prefix, _BF16, 8, dev)
+        Np = kp_size[1]
+        if kp_size != vp_size or kp_size != (1, Np, Hk, d):
             raise ValueError("k_prefix and v_prefix must be [Np, Hk, d] with the heads and head dimension of k")
-        a.k_prefix, a.v_prefix = k_prefix.data_ptr(), v_prefix.data_ptr()
-        a.k_prefix_stride, a.v_prefix_stride = _strides(k_prefix), _strides(v_prefix)
+    spans_at, span_batches = 0, 1
     if spans is not None:
-        if (spans.dtype != torch.int32 or spans.device != dev or not spans.is_contiguous()
-                or tuple(spans.shape) not in ((Nq, 2), (1, Nq, 2), (B, Nq, 2))):
+        size = spans.shape
+        if (spans.dtype != torch.int32 or spans.get_device() != dev or not spans.is_contiguous()
+                or size[-2:] != (Nq, 2) or len(size) > 3 or (len(size) == 3 and size[0] not in (1, B))):
             raise ValueError("spans must be a contiguous int32 tensor [Nq, 2] or [B, Nq, 2] on the device of q")
-        a.spans, a.span_batches = spans.data_ptr(), spans.shape[0] if spans.dim() == 3 else 1
+        spans_at, span_batches = spans.data_ptr(), size[0] if len(size) == 3 else 1
     cap = float(cap or 0.0)
     if not 0.0 <= cap < math.inf:
         raise ValueError("cap must be a non-negative number (0: no cap)")
-    a.cap, a.scale = cap, float(scale or 0.0)
-    a.pos_batches = 1
+    slopes_at, pos_at, pos_batches, pp_at = 0, [0, 0], 1, 0
     if slopes is not None:
-        if slopes.dtype != torch.float32 or not slopes.is_contiguous() or slopes.device != dev or tuple(slopes.shape) != (H,):
+        if slopes.dtype != torch.float32 or not slopes.is_contiguous() or slopes.get_device() != dev or slopes.shape != (H,):
             raise ValueError("slopes must be a contiguous fp32 tensor [H] on the device of q")
-        a.slopes = slopes.data_ptr()
-        for name, t, n in (("q_pos", q_pos, Nq), ("k_pos", k_pos, Nk)):
+        slopes_at = slopes.data_ptr()
+        for x, (name, t, n) in enumerate((("q_pos", q_pos, Nq), ("k_pos", k_pos, Nk))):
             if t is None:
                 continue
-            if (t.dtype != torch.float32 or not t.is_contiguous() or t.device != dev
+            if (t.dtype != torch.float32 or not t.is_contiguous() or t.get_device() != dev
                     or tuple(t.shape) not in ((n,), (1, n), (B, n))):
                 raise ValueError(f"{name} must be a contiguous fp32 tensor [N] or [B, N] on the device of q")
             batches = t.shape[0] if t.dim() == 2 else 1
             if q_pos is not None and k_pos is not None and batches != (q_pos.shape[0] if q_pos.dim() == 2 else 1):
                 raise ValueError("q_pos and k_pos must both be for one or both for all batch entries")
-            a.pos_batches = batches
-            setattr(a, name, t.data_ptr())
+            pos_batches, pos_at[x] = batches, t.data_ptr()
         if prefix_pos is not None:
-            if (prefix_pos.dtype != torch.float32 or not prefix_pos.is_contiguous() or prefix_pos.device != dev
+            if (prefix_pos.dtype != torch.float32 or not prefix_pos.is_contiguous() or prefix_pos.get_device() != dev
                     or tuple(prefix_pos.shape) != (Np,)):
                 raise ValueError("prefix_pos must be a contiguous fp32 tensor [Np] on the device of q")
-            a.prefix_pos = prefix_pos.data_ptr()
+            pp_at = prefix_pos.data_ptr()
     elif q_pos is not None or k_pos is not None or prefix_pos is not None:
         raise ValueError("positions belong to slopes")
+    given = o is not None or lse is not None
     if o is None:
-        o = _new((B, Nq, H, d), torch.bfloat16, dev, stream)
+        o = _new(q, (B, Nq, H, d), torch.bfloat16, stream)
     if lse is None and return_lse:
-        lse = _new((B, H, Nq), torch.float32, dev, stream)
-    _check_outputs(q, o, lse)
-    a.o, a.lse = o.data_ptr(), _ptr(lse)
-    a.B, a.Nq, a.Nk, a.Np, a.H, a.Hk, a.d = B, Nq, Nk, Np, H, Hk, d
-    _call_on(fn, a, dev, stream)
+        lse = _new(q, (B, H, Nq), torch.float32, stream)
+    if given:
+        _check_outputs(q, o, lse)
+    args = _SPAN_ARGS.pack(q_at, k_at, v_at, kp_at, vp_at, o.data_ptr(), 0 if lse is None else lse.data_ptr(), spans_at,
+                           slopes_at, pos_at[0], pos_at[1], pp_at, qs[0], qs[1], qs[2], ks[0], ks[1], ks[2], vs[0],
+                           vs[1], vs[2], kps[0], kps[1], kps[2], vps[0], vps[1], vps[2], B, Nq, Nk, Np, H, Hk, d,
+                           span_batches, pos_batches, float(scale or 0.0), cap)
+    _call_on(fn, args, dev, stream)
     return o, lse
 
 
