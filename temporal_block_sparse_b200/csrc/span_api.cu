@@ -227,8 +227,13 @@ double plan_us(const Plan& pl, int d, int64_t slots) {
   if (np == 0 || no == 0)
     us = double(ceil_div(np + no, slots)) * std::max(tp, to);
   else
-    us = std::max(std::max(tp, to), (double(np) * tp + double(no) * to) / double(slots) + std::max(tp, to) * 0.5);
-  return us + (pl.parts ? 5.0 : 0.0);  // the join: its launch and the parts' way through L2
+    us = std::max(std::max(tp, to), (double(np) * tp + double(no) * to) / double(slots) + to * 0.5);
+  if (pl.parts) {
+    // the join: its launch, scratch and the parts' way through L2; passes of two kinds take a launch each
+    const double rows = 128.0 * 2.0 * (double(np) + double(no));
+    us += 8.0 + rows * (d * 4 + 8) * 2.0 / 4e6 + (np && no && pl.pre.F != pl.own.F ? 4.0 : 0.0);
+  }
+  return us;
 }
 
 // Splits the key ranges where that shortens the plan: few items leave SMs idle, and one long item
@@ -338,7 +343,7 @@ bool make_maps(const lite_span_args& a, int Np, const DeviceContext& dc, const P
   return true;
 }
 
-lite::SpanPass kernel_pass(const PassPlan& ps, int64_t slot0) {
+lite::SpanPass kernel_pass(const PassPlan& ps, int64_t slot0, int64_t slots) {
   lite::SpanPass k;
   k.items = int(ps.items());
   k.pairs = int(ps.pairs);
@@ -347,6 +352,7 @@ lite::SpanPass kernel_pass(const PassPlan& ps, int64_t slot0) {
   k.TN = ps.TN;
   k.per_item = ps.F == 4 ? 1 : 2;
   k.slot0 = int(slot0);
+  k.tail = int(std::min(ps.units, ceil_div(2 * slots, std::max<int64_t>(ps.pairs * ps.splits, 1))));
   return k;
 }
 
@@ -387,13 +393,22 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   p.k_bm = a.B > 1 && a.k_stride[0] != 0;
   p.v_bm = a.B > 1 && a.v_stride[0] != 0;
   p.fused = !pl.stacked;
-  p.pre = kernel_pass(pl.pre, 0);
-  p.own = kernel_pass(pl.own, pl.pre.items() * p.pre.per_item);
+  p.pre = kernel_pass(pl.pre, 0, slots);
+  p.own = kernel_pass(pl.own, pl.pre.items() * p.pre.per_item, slots);
   const float scale = (a.scale > 0.f && !std::isnan(a.scale)) ? a.scale : 1.0f / std::sqrt(float(a.d));
   p.scale_log2 = scale * 1.4426950408889634f;
   if (a.cap > 0.f) {
     p.cap_a = 2.f * p.scale_log2 / a.cap;
     p.cap_c = a.cap * 1.4426950408889634f;
+    // tanh(z) / z on |z| <= 0.6 as a polynomial in z^2: the least largest relative error (7.3e-8) of
+    // degree 4, fitted numerically; z = s scale / cap
+    const double c[5] = {0.999999927, -0.3333231, 0.133101736, -0.0521014795, 0.0154754266};
+    const double zs = double(scale) / a.cap;
+    // (and not so large that a row's reference, the largest |score|, is far from its maximum: 24 in log2 units)
+    p.cap_mid = float(0.6 / zs);
+    p.cap_near = float(std::min(0.6 / zs, 24.0 / (double(scale) * 1.4426950408889634)));
+    double f = double(scale) * 1.4426950408889634;
+    for (int x = 0; x < 5; ++x, f *= zs * zs) p.cap_b[x] = float(c[x] * f);
   }
   // Scratch: work counters where there are more items than CTAs (their lengths depend on the spans), and
   // the parts.

@@ -39,6 +39,13 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
+// max(|a|, |b|, |c|)
+__device__ __forceinline__ float abs_max3(float a, float b, float c) {
+  float y;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+
 constexpr int kSpanCap = 1, kSpanBias = 2;  // MOD bits of the kernel
 
 // One pass over query tiles: the prefix pass (tokens of the whole batch against the shared prefix) or
@@ -51,6 +58,7 @@ struct SpanPass {
   int TN;                   // tokens of a query tile: 128 / G, or 32 / G (F = 4)
   int per_item;             // parts an item writes: 1 (F = 4) or 2
   int slot0;                // index of the pass's first part
+  int tail;                 // last units, whose items are handed out together
 };
 
 struct SpanParams {
@@ -76,6 +84,9 @@ struct SpanParams {
   int n_items;              // pre.items + own.items of this launch
   float scale_log2;         // softmax scale * log2(e)
   float cap_a, cap_c;       // 2 scale log2(e) / cap and cap log2(e)
+  float cap_mid;            // the polynomial holds for scores (before scale) up to this: 0.6 cap
+  float cap_near;           // and a tile of scores up to this takes the fast path
+  float cap_b[5];           // its coefficients in s^2
 };
 
 // floats of one part: O rows, then row maxima and row sums of a 128-row tile
@@ -134,15 +145,25 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
   const bool prefix = idx < p.pre.items;
   const SpanPass& ps = prefix ? p.pre : p.own;
   const int i = prefix ? idx : idx - p.pre.items;
-  const int per = ps.pairs * ps.splits, unit = i / per, rem = i - unit * per;
+  // The last rows first: where rows see their past, these have the most keys. Units one after the other,
+  // so that the CTAs at work share keys and values in L2; but the last `tail` units (about two items a
+  // CTA) interleaved, for long items started at the very end would keep a few CTAs busy alone.
+  const int units = prefix ? p.Hk : p.B * p.Hk, per = ps.pairs * ps.splits;
+  int unit = i / per, rem = i - unit * per;
+  int rank = rem / ps.splits;
+  if (unit >= units - ps.tail) {
+    rem = i - (units - ps.tail) * per;
+    rank = rem / (ps.tail * ps.splits);
+    rem -= rank * (ps.tail * ps.splits);
+    unit = units - ps.tail + rem / ps.splits;
+  }
   const int split = rem % ps.splits;
-  // the last rows first: where rows see their past, these have the most keys
-  const int pair = ps.pairs - 1 - rem / ps.splits;
+  const int pair = ps.pairs - 1 - rank;
   it.kind = prefix ? 1 : 0;
   it.alt = ps.alt;
   it.b = prefix ? 0 : unit / p.Hk;
   it.hk = prefix ? unit : unit - it.b * p.Hk;
-  it.slot = ps.slot0 + i * ps.per_item;
+  it.slot = ps.slot0 + ((unit * ps.pairs + rank) * ps.splits + split) * ps.per_item;
   const int ntok = prefix ? p.B * p.Nq : p.Nq;
   const int tp = (prefix || p.fused) ? p.Tp : 0;
   int jlo = 0x7fffffff, jhi = 0;  // own key tiles that either query tile has to see
@@ -545,108 +566,84 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       }
       float m_used = -INFINITY;  // exponent reference (lazy rescale), log2 units
       float l = 0.f;             // row sum relative to m_used
+      // given position of key r of the group's tile idx
+      auto key_pos = [&](int idx) -> float {
+        const int entry = mt->q0 + idx * mt->step;
+        const bool pre = entry < mt->n_pre;
+        const int m = (pre ? it->v_first + entry : mt->j_first + entry - mt->n_pre) * BN + r;
+        const float* at = pre ? p.p_pos : p.k_pos;
+        if (!at || r >= BN || m >= (pre ? p.Np : p.Nk)) return 0.f;
+        return __ldg(at + (pre ? 0 : it->b * p.k_pos_b) + m);
+      };
+      float kp_next = 0.f;
+      if (BIAS && n_live > 0) kp_next = key_pos(0);
       for (int idx = 0; idx < n_live; ++idx) {
         const int entry = mt->q0 + idx * mt->step;
         const bool pre = entry < mt->n_pre;
         const int j0 = (pre ? it->v_first + entry : mt->j_first + entry - mt->n_pre) * BN;  // the tile's first key
         float* kp = kpos + (idx & 1) * BN;
-        if (BIAS) {
-          // thread r brings the position of key r; the buffer's last readers passed the barrier of
-          // the tile before
-          if (r < BN) {
-            const int m = j0 + r;
-            float x = 0.f;
-            if (pre) {
-              if (m < p.Np) x = p.p_pos ? __ldg(p.p_pos + m) : float(m);
-            } else {
-              if (m < p.Nk) x = p.k_pos ? __ldg(p.k_pos + it->b * p.k_pos_b + m) : float(p.Np + m);
-            }
-            kp[r] = x;
-          }
+        const bool given = BIAS && (pre ? p.p_pos : p.k_pos) != nullptr;
+        if (given) {
+          // thread r brings the position of key r (read a tile ahead); the buffer's last readers passed
+          // the barrier of the tile before
+          if (r < BN) kp[r] = kp_next;
           ptx::named_bar_sync(gbar, 128);
         }
+        if (BIAS && idx + 1 < n_live) kp_next = key_pos(idx + 1);
         wt.wait(BAR(s_full[grp]), tg & 1);
         ++tg;
         __syncwarp();
         ptx::tc_fence_after();
         if (warp_valid) {
-          uint32_t sr[NC];
-          if constexpr (NC >= 32) {
-#pragma unroll
-            for (int c = 0; c < NC / 32; ++c)
-              ptx::tmem_ld32(s_tmem + col0 + c * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[c * 32]));
-          } else {
-            tmem_ld16(s_tmem + col0, sr);
-          }
-          ptx::tmem_wait_ld();
-          float s[NC];
-#pragma unroll
-          for (int x = 0; x < NC; ++x) s[x] = __uint_as_float(sr[x]);
-          if (CAP) {
-            // cap tanh(z) = cap - 2 cap / (1 + e^{2z}), in log2 units; both ends saturate exactly
-#pragma unroll
-            for (int x = 0; x < NC; ++x)
-              s[x] = fmaf(-2.f * p.cap_c, fast_rcp(1.f + ptx::ex2(s[x] * p.cap_a)), p.cap_c);
-          }
-          if (BIAS) {
-#pragma unroll
-            for (int x = 0; x < NC; x += 4) {
-              const float4 k4 = *reinterpret_cast<const float4*>(kp + col0 + x);
-              const float dd[4] = {k4.x - qp, k4.y - qp, k4.z - qp, k4.w - qp};
-#pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const float base = CAP ? s[x + y] : s[x + y] * p.scale_log2;
-                s[x + y] = fmaf(-slope, fabsf(dd[y]), base);
-              }
-            }
-          }
+          constexpr int PC = NC < 32 ? NC : 32;  // columns loaded, converted and stored at a time
+          const auto load_scores = [&](int c, float (&v)[PC]) {
+            if constexpr (PC == 32)
+              ptx::tmem_ld32(s_tmem + col0 + c * 32, reinterpret_cast<uint32_t(&)[32]>(v));
+            else
+              tmem_ld16(s_tmem + col0, reinterpret_cast<uint32_t(&)[16]>(v));
+          };
           // columns [lo, hi) of the tile are keys that this row sees
           const int lo = pre ? 0 : ks - j0, hi = pre ? p.Np - j0 : ke - j0;
           const bool masked = pre ? hi < BN : (mt->full_lo > j0 || mt->full_hi < j0 + BN);
-          if (masked) {
-            // each half-word of 32 columns as a bit mask, then one select per column
+          // the keys seen among columns col0 + 32 c and on, as bits: one select per column then
+          const auto seen = [&](int c) -> uint32_t {
+            const int at = col0 + 32 * c;
+            const int a = min(max(lo - at, 0), 32), z = min(max(hi - at, 0), 32);
+            const uint32_t upto = z >= 32 ? 0xffffffffu : ((1u << z) - 1u);
+            const uint32_t below = a >= 32 ? 0xffffffffu : ((1u << a) - 1u);
+            return upto & ~below;
+          };
+          const auto row_max = [](const auto& v, int n, float (&m)[4]) {
 #pragma unroll
-            for (int c = 0; c < (NC + 31) / 32; ++c) {
-              const int at = col0 + 32 * c;
-              const int a = min(max(lo - at, 0), 32), z = min(max(hi - at, 0), 32);
-              const uint32_t upto = z >= 32 ? 0xffffffffu : ((1u << z) - 1u);
-              const uint32_t below = a >= 32 ? 0xffffffffu : ((1u << a) - 1u);
-              const uint32_t bits = upto & ~below;
-#pragma unroll
-              for (int x = 0; x < (NC < 32 ? NC : 32); ++x)
-                s[32 * c + x] = (bits & (1u << x)) ? s[32 * c + x] : -INFINITY;
+            for (int x = 0; x < n; x += 8) {
+              m[0] = ptx::fmax3(m[0], v[x], v[x + 1]);
+              m[1] = ptx::fmax3(m[1], v[x + 2], v[x + 3]);
+              m[2] = ptx::fmax3(m[2], v[x + 4], v[x + 5]);
+              m[3] = ptx::fmax3(m[3], v[x + 6], v[x + 7]);
             }
-          }
-          float m0 = -INFINITY, m1 = -INFINITY, m2 = -INFINITY, m3 = -INFINITY;
-#pragma unroll
-          for (int x = 0; x < NC; x += 8) {
-            m0 = ptx::fmax3(m0, s[x], s[x + 1]);
-            m1 = ptx::fmax3(m1, s[x + 2], s[x + 3]);
-            m2 = ptx::fmax3(m2, s[x + 4], s[x + 5]);
-            m3 = ptx::fmax3(m3, s[x + 6], s[x + 7]);
-          }
-          const float to_log2 = MOD ? 1.f : p.scale_log2;
-          const float loc = ptx::fmax3(m0, m1, fmaxf(m2, m3)) * to_log2;
-          const bool need = loc > m_used + kRescaleLog2;
+          };
+          const auto all4 = [](const float (&m)[4]) { return ptx::fmax3(m[0], m[1], fmaxf(m[2], m[3])); };
+          float loc = -INFINITY;  // the tile's row maximum, or a reference near it (log2 units)
+          // lazy rescale of the accumulator, as in lite_attn_kernel
+          bool need = false;
           float alpha = 1.f;
-          if (need) {
-            alpha = ptx::ex2(m_used - loc);
-            m_used = loc;
-            l *= alpha;
-          }
-          // a row that has seen no key yet keeps m_used = -inf; its exponents are -inf - 0
-          const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
-          const float2 sc2 = make_float2(to_log2, to_log2);
-          const float2 nm2 = make_float2(neg_m, neg_m);
+          const auto take_reference = [&]() {
+            need = loc > m_used + kRescaleLog2;
+            if (need) {
+              alpha = ptx::ex2(m_used - loc);
+              m_used = loc;
+              l *= alpha;
+            }
+            // a row that has seen no key yet keeps m_used = -inf; its exponents are -inf - 0
+            return m_used == -INFINITY ? 0.f : -m_used;
+          };
           float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          constexpr int PC = NC < 32 ? NC : 32;  // columns converted and stored at a time
-#pragma unroll
-          for (int c = 0; c < NC / PC; ++c) {
+          // P = 2^(exponent) of chunk c's column pairs, in bf16 over S columns that have been read
+          const auto put_p = [&](int c, auto exponent) {
             uint32_t pk[PC / 2];
 #pragma unroll
             for (int x = 0; x < PC / 2; ++x) {
-              const float2 sx = make_float2(s[PC * c + 2 * x], s[PC * c + 2 * x + 1]);
-              const float2 a = MOD ? __fadd2_rn(sx, nm2) : __ffma2_rn(sx, sc2, nm2);
+              const float2 a = exponent(2 * x);
               const float2 pp = make_float2(ptx::ex2(a.x), ptx::ex2(a.y));
               acc[x & 3] = __fadd2_rn(acc[x & 3], pp);
               __nv_bfloat162 h2 = __floats2bfloat162_rn(pp.x, pp.y);
@@ -656,6 +653,152 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
               ptx::tmem_st16(s_tmem + col0 / 2 + c * 16, pk);
             else
               ptx::tmem_st8(s_tmem + col0 / 2, pk);
+          };
+          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+          if constexpr (MOD == 0) {
+            // the row is read once and stays in registers for the maximum and the exponentials
+            float v[NC / PC][PC];
+#pragma unroll
+            for (int c = 0; c < NC / PC; ++c) load_scores(c, v[c]);
+            ptx::tmem_wait_ld();
+            if (masked) {
+#pragma unroll
+              for (int c = 0; c < NC / PC; ++c) {
+                const uint32_t bits = seen(c);
+#pragma unroll
+                for (int x = 0; x < PC; ++x) v[c][x] = (bits & (1u << x)) ? v[c][x] : -INFINITY;
+              }
+            }
+            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < NC / PC; ++c) row_max(v[c], PC, m);
+            loc = all4(m) * p.scale_log2;
+            const float neg_m = take_reference();
+            const float2 nm2 = make_float2(neg_m, neg_m);
+#pragma unroll
+            for (int c = 0; c < NC / PC; ++c)
+              put_p(c, [&](int x) { return __ffma2_rn(make_float2(v[c][x], v[c][x + 1]), sc2, nm2); });
+          } else {
+            // Key x of the tile (default positions) is at distance |base + x|; where all rows of the warp have
+            // the tile on one side, the bias is linear in x: sg * (base + x).
+            const float base = BIAS ? float(j0 + col0 + (pre ? 0 : p.Np)) - qp : 0.f;
+            const float sg = base < 0.f ? slope : -slope;
+            // The exponents of a row need a reference near its maximum, not the maximum: P has the same
+            // relative precision at every scale. Here it is at most 2 * 24 + 30 above (the largest |score|
+            // taken for the score under a cap, the bias's spread over 32 columns; 60 without a cap), and 2^-78
+            // is far from the end of the range. So a tile that needs no mask takes it from the raw scores, and the cap and the bias
+            // are packed products inside the exponent. The scores are read from TMEM twice, 32 at a time: a
+            // whole row in registers left too few of them to keep these longer chains apart.
+            bool fast = !masked && !given;
+            if (BIAS)
+              fast = fast && __all_sync(0xffffffffu, !valid || ((base >= 0.f || base <= 1.f - NC) &&
+                                                                 fabsf(slope) * PC <= (CAP ? 30.f : 60.f)));
+            float v[2][PC];
+            if (fast) {
+              float top = -INFINITY;
+              load_scores(0, v[0]);
+#pragma unroll
+              for (int c = 0; c < NC / PC; ++c) {
+                ptx::tmem_wait_ld();
+                if (c + 1 < NC / PC) load_scores(c + 1, v[(c + 1) & 1]);
+                float m[4];
+                if constexpr (CAP) {
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) m[x] = 0.f;
+#pragma unroll
+                  for (int x = 0; x < PC; x += 2) m[(x >> 1) & 3] = abs_max3(m[(x >> 1) & 3], v[c & 1][x], v[c & 1][x + 1]);
+                } else {
+#pragma unroll
+                  for (int x = 0; x < 4; ++x) m[x] = -INFINITY;
+                  row_max(v[c & 1], PC, m);
+                }
+                const float here = all4(m);
+                top = fmaxf(top, here);
+                // (the cap only lowers a score; the bias is largest at one end of the chunk)
+                if (BIAS)
+                  loc = fmaxf(loc, fmaf(here, p.scale_log2, fmaxf(sg * (base + float(PC * c)), sg * (base + float(PC * c + PC - 1)))));
+              }
+              if (CAP) fast = !__any_sync(0xffffffffu, valid && !(top <= p.cap_near));
+              if (!BIAS) loc = top * p.scale_log2;
+            }
+            if (fast) {
+              const float neg_m = take_reference();
+              // bias minus reference of columns 2y, 2y + 1 of each eight, stepped from one eight to the next
+              // (at most 16 sums: off by 2^-20 of an exponent that matters)
+              float2 w[4];
+              const float c0 = fmaf(sg, base, neg_m);
+#pragma unroll
+              for (int y = 0; y < 4; ++y)
+                w[y] = BIAS ? make_float2(fmaf(sg, float(2 * y), c0), fmaf(sg, float(2 * y + 1), c0))
+                            : make_float2(neg_m, neg_m);
+              const float2 sg8 = make_float2(8.f * sg, 8.f * sg);
+              load_scores(0, v[0]);
+#pragma unroll
+              for (int c = 0; c < NC / PC; ++c) {
+                ptx::tmem_wait_ld();
+                if (c + 1 < NC / PC) load_scores(c + 1, v[(c + 1) & 1]);
+                put_p(c, [&](int x) {
+                  const float2 a = make_float2(v[c & 1][x], v[c & 1][x + 1]);
+                  float2& wx = w[(x >> 1) & 3];
+                  const float2 add = wx;
+                  if (BIAS) wx = __fadd2_rn(wx, sg8);
+                  if constexpr (CAP) {
+                    // cap tanh(s scale / cap) as an odd polynomial: two exponential-unit operations a score
+                    // more would triple the work of the unit that bounds the kernel
+                    const float2 y = __fmul2_rn(a, a);
+                    float2 t = __ffma2_rn(make_float2(p.cap_b[4], p.cap_b[4]), y, make_float2(p.cap_b[3], p.cap_b[3]));
+                    t = __ffma2_rn(t, y, make_float2(p.cap_b[2], p.cap_b[2]));
+                    t = __ffma2_rn(t, y, make_float2(p.cap_b[1], p.cap_b[1]));
+                    t = __ffma2_rn(t, y, make_float2(p.cap_b[0], p.cap_b[0]));
+                    return __ffma2_rn(a, t, add);
+                  } else {
+                    return __ffma2_rn(a, sc2, add);
+                  }
+                });
+              }
+            } else {
+              // Tiles that a span ends in, scores near the cap, tiles on both sides of their rows, given
+              // positions: every score in full, back into TMEM, then the exponentials.
+              loc = -INFINITY;
+              float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+              for (int c = 0; c < NC / PC; ++c) {
+                load_scores(c, v[0]);
+                ptx::tmem_wait_ld();
+                const uint32_t bits = seen(c);
+                const float at = base + float(32 * c);
+                const float* kc = kp + col0 + 32 * c;
+#pragma unroll
+                for (int x = 0; x < PC; ++x) {
+                  float t = v[0][x] * p.scale_log2;
+                  if (CAP) {
+                    // cap tanh(z) = cap - 2 cap / (1 + e^{2z}), in log2 units; both ends saturate exactly.
+                    // Near zero it cancels (a large cap against small scores), and the polynomial takes over.
+                    const float y = v[0][x] * v[0][x];
+                    const float far = fmaf(-2.f * p.cap_c, fast_rcp(1.f + ptx::ex2(v[0][x] * p.cap_a)), p.cap_c);
+                    t = v[0][x] * fmaf(fmaf(fmaf(fmaf(p.cap_b[4], y, p.cap_b[3]), y, p.cap_b[2]), y, p.cap_b[1]), y, p.cap_b[0]);
+                    t = fabsf(v[0][x]) <= p.cap_mid ? t : far;
+                  }
+                  if (BIAS) t = fmaf(-slope, fabsf(given ? kc[x] - qp : at + float(x)), t);
+                  v[0][x] = (!masked || (bits & (1u << x))) ? t : -INFINITY;
+                }
+                row_max(v[0], PC, m);
+                if constexpr (PC == 32)
+                  ptx::tmem_st32(s_tmem + col0 + c * 32, reinterpret_cast<uint32_t(&)[32]>(v[0]));
+                else
+                  ptx::tmem_st16(s_tmem + col0, reinterpret_cast<uint32_t(&)[16]>(v[0]));
+              }
+              ptx::tmem_wait_st();
+              loc = all4(m);
+              const float neg_m = take_reference();
+              const float2 nm2 = make_float2(neg_m, neg_m);
+#pragma unroll 1
+              for (int c = 0; c < NC / PC; ++c) {
+                load_scores(c, v[0]);
+                ptx::tmem_wait_ld();
+                put_p(c, [&](int x) { return __fadd2_rn(make_float2(v[0][x], v[0][x + 1]), nm2); });
+              }
+            }
           }
           if constexpr (F > 1) {
             // the other quarters of the row's keys are another lane's: P = 0 there

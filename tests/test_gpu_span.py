@@ -124,3 +124,36 @@ def test_prefix(d, B, Nq, Nk, Np, H, Hk):
             got = la.lite_attn_prefix(q, kp, vp, k, v, spans, **kw)
             rk = {x: f64(y) if isinstance(y, torch.Tensor) else y for x, y in kw.items()}
             check(got, ref.span_attention(f64(q), f64(k), f64(v), f64(spans), f64(kp), f64(vp), **rk))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 40, 300])
+@pytest.mark.parametrize("batches", [1, 2])
+def test_given_positions(d, Nq, batches):
+    B, Nk, Np, H = 2, 300, 150, 2
+    q, k, v, kp, vp = make(Nq, (B, Nq, H, d), (B, Nk, H, d), (B, Nk, H, d), (Np, H, d), (Np, H, d))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(d)
+    slopes = torch.tensor([0.3, 0.01], device="cuda")
+    qpos = torch.randint(0, 50, (batches, Nq), generator=g, device="cuda").float()  # e.g. frame numbers
+    kpos = torch.randint(0, 50, (batches, Nk), generator=g, device="cuda").float()
+    ppos = torch.randint(-20, 20, (Np,), generator=g, device="cuda").float() + 0.5
+    for some in ({"q_pos": qpos, "k_pos": kpos}, {"k_pos": kpos}, {"q_pos": qpos}):
+        for cap in (0.0, 4.0):
+            rk = {x: f64(y) for x, y in some.items()}
+            got = la.lite_attn_span(q, k, v, slopes=slopes, cap=cap, **some)
+            check(got, ref.span_attention(f64(q), f64(k), f64(v), slopes=f64(slopes), cap=cap, **rk))
+    spans = sp.padded_spans([Nk, 33], Nq)
+    got = la.lite_attn_prefix(q, kp, vp, k, v, spans, slopes=slopes, q_pos=qpos, k_pos=kpos, prefix_pos=ppos)
+    check(got, ref.span_attention(f64(q), f64(k), f64(v), f64(spans), f64(kp), f64(vp), slopes=f64(slopes),
+                                  q_pos=f64(qpos), k_pos=f64(kpos), prefix_pos=f64(ppos)))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap", [1e-3, 0.5, 3.0, 30.0, 1e6])
+def test_caps_from_saturated_to_idle(d, cap):
+    # scores reach +-20 here: the smaller caps saturate, the largest change nothing. 32-bit scores of
+    # size 20 are good to 20 * 2^-20 after the cap's arithmetic; the bounds of check() hold unchanged.
+    q, k, v = make(11, (1, 150, 2, d), (1, 200, 2, d), (1, 200, 2, d), gain=2.2)
+    got = la.lite_attn_span(q, k, v, sp.padded_spans([170], 150), cap=cap)
+    check(got, ref.span_attention(f64(q), f64(k), f64(v), f64(sp.padded_spans([170], 150)), cap=cap))
