@@ -378,6 +378,10 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   p.Tp = Tp;
   p.o = static_cast<__nv_bfloat16*>(a.o);
   p.lse = a.lse;
+  p.v = static_cast<const __nv_bfloat16*>(a.v);
+  p.v_stride[0] = a.B > 1 ? a.v_stride[0] : 0;
+  p.v_stride[1] = a.Nk > 1 ? a.v_stride[1] : 0;
+  p.v_stride[2] = a.Hk > 1 ? a.v_stride[2] : 0;
   p.spans = a.spans;
   p.span_b = a.span_batches > 1 ? 2ll * a.Nq : 0;
   p.slopes = a.slopes;

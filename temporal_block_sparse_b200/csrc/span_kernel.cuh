@@ -61,9 +61,13 @@ struct SpanPass {
   int tail;                 // last units, whose items are handed out together
 };
 
+constexpr int kSpanBad = 5;  // key tiles with non-finite values that an item lists
+
 struct SpanParams {
   __nv_bfloat16* o;         // [B, Nq, H, D]
   float* lse;               // [B, H, Nq] or null
+  const __nv_bfloat16* v;   // [B, Nk, Hk, D] and its strides (batch, token, head), for the repair of rows
+  long long v_stride[3];
   const int* spans;         // [B or 1, Nq, 2] or null (all keys)
   long long span_b;         // 2 * Nq, or 0: one table for all batch entries
   const float* slopes;      // [H] (bias)
@@ -112,8 +116,50 @@ struct SpanInfo {
   int b, hk;
   int slot;              // index of its first part in scratch
   int v_first;
+  uint32_t u0;           // union index of its first tile
+  int clean0, clean1;    // every row sees all keys of the own tiles [clean0, clean1)
+  int n_bad;             // own key tiles whose non-finite values were taken out of shared memory (see
+  int bad[kSpanBad];     // span_clean), the first kSpanBad of them by index
   SpanTile t[2];
 };
+
+// Whether some row of the item may not see all keys of own key tile j (the same answer for both groups and the
+// producer; a tile that only one query tile computes may be counted for the other's sake).
+__device__ __forceinline__ bool span_mixed(const SpanInfo& it, int j) { return j < it.clean0 || j >= it.clean1; }
+
+// Place of own key tile j (entry q of its list) among the item's union tiles.
+__device__ __forceinline__ int span_union(const SpanInfo& it, int j, int q) {
+  if (it.alt) return q;
+  const SpanTile& a = it.t[0];
+  const SpanTile& b = it.t[1];
+  const int na = a.n_live - a.n_pre, nb = b.n_live - b.n_pre;
+  const int both = max(0, min(a.j_first + na, b.j_first + nb) - max(a.j_first, b.j_first));
+  return max(a.n_pre, b.n_pre) + min(max(j - a.j_first, 0), na) + min(max(j - b.j_first, 0), nb) -
+         min(max(j - max(a.j_first, b.j_first), 0), both);
+}
+
+// Zeroes the infinities and NaN among this thread's 16-byte pieces of a V tile (pieces first, first + step,
+// ..); true if there were any.
+__device__ __forceinline__ bool span_clean(uint8_t* tile, int first, int step, int pieces) {
+  uint32_t most = 0u;  // largest magnitude of either half-word
+  for (int i = first; i < pieces; i += step) {
+    const uint4 x = *reinterpret_cast<const uint4*>(tile + i * 16);
+    most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+  }
+  if ((most & 0xffffu) < 0x7f80u && (most >> 16) < 0x7f80u) return false;
+  for (int i = first; i < pieces; i += step) {
+    uint32_t* x = reinterpret_cast<uint32_t*>(tile + i * 16);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      uint32_t w = x[y];
+      if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+      if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+      x[y] = w;
+    }
+  }
+  return true;
+}
 
 struct alignas(8) SpanCtl {
   uint64_t q_full, q_empty;
@@ -215,6 +261,15 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
     }
   }
   if (jhi == 0) jlo = 0;
+  int clo = 0, chi = p.Nk;
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+    if (thi[g] > tlo[g]) {
+      clo = max(clo, it.t[g].full_lo);
+      chi = min(chi, it.t[g].full_hi);
+    }
+  it.clean0 = clo / BN + (clo % BN != 0);
+  it.clean1 = chi == p.Nk ? 0x7fffffff : chi / BN;
   // virtual tiles: prefix [0, tp), then own jlo .. jhi; this split's are [v0, v1)
   const long long total = tp + (jhi - jlo);
   const int v0 = int(total * split / ps.splits), v1 = int(total * (split + 1) / ps.splits);
@@ -232,6 +287,30 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
   }
 }
 
+// This thread's part in cleaning own key tile j (entry q of its group's list): both groups have a half of it each
+// when both compute it.
+template <typename C, int BN>
+__device__ __noinline__ void span_clean_tile(SpanCtl* ctl, uint8_t* smem, const Waiter& wt, int slot, int grp, int tid,
+                                             int j, int q) {
+  SpanInfo& it = ctl->info[slot];
+  const uint32_t u = it.u0 + span_union(it, j, q);
+  const SpanTile& other = it.t[grp ^ 1];
+  const bool both = !it.alt && j >= other.j_first && j < other.j_first + other.n_live - other.n_pre;
+  wt.wait(ptx::smem_addr(&ctl->kv_full[(u + 1) & 1]), ((u + 1) >> 1) & 1);  // V_u comes with bundle u + 1
+  if (!span_clean(smem + C::OFF_V + (u & 1) * C::KV_BYTES, both ? grp * 128 + tid : tid, both ? 256 : 128,
+                  C::KV_BYTES / 16))
+    return;
+  ptx::fence_proxy_async_smem();
+  for (int x = 0; x < kSpanBad; ++x) {
+    const int old = atomicCAS(&it.bad[x], -1, j);
+    if (old == -1 || old == j) {
+      atomicMax(&it.n_bad, x + 1);
+      return;
+    }
+  }
+  atomicMax(&it.n_bad, kSpanBad + 1);
+}
+
 // Shared memory: lite_attn_kernel's layout, with a staging area of 32 rows x 128 bytes a softmax warp.
 template <int D, int BN>
 struct SpanCfg : AttnCfg<D, BN> {
@@ -244,7 +323,8 @@ struct SpanCfg : AttnCfg<D, BN> {
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
-constexpr uint32_t kSpanAlt = 2048u;  // ring word: both groups use the first query tile
+constexpr uint32_t kSpanAlt = 2048u;    // ring word: both groups use the first query tile
+constexpr uint32_t kSpanCheck = 4096u;  // V may be cleaned by either group before any of its products
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -351,7 +431,11 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       SpanInfo it;
       it.kind = -1;
       if (item >= 0) span_decode<BN>(p, item, lane, it);
+      it.n_bad = 0;
+#pragma unroll
+      for (int x = 0; x < kSpanBad; ++x) it.bad[x] = -1;
       if (lane == 0) {
+        it.u0 = u;
         ctl->info[slot] = it;
         ptx::mbar_arrive(BAR(item_full[slot]));
       }
@@ -414,6 +498,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
                 ++d1;
               }
               if (d0 == n0 && d1 == n1) f |= kItemLast;
+              if (!pre && span_mixed(it, j)) f |= kSpanCheck;
               ok = bundle(true, pre, j, it.hk, it.b, f);
               f = 0u;
             }
@@ -490,6 +575,13 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           ptx::mma_commit(BAR(s_full[g]));
           return true;
         };
+        if (prev & kSpanCheck) {
+          // either group may still be cleaning V: both have to be done with the tile
+#pragma unroll
+          for (int g = 0; g < 2; ++g)
+            if (ok && (prev & (kLive0 << g))) ok = wt.wait(BAR(p_full[g]), pc[g] & 1);
+          if (!ok) break;
+        }
         if (prev & f & (kLive0 | kLive1)) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
@@ -829,10 +921,44 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           const float2 acc2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
           l += acc2.x + acc2.y;
         }
+        if (!pre && span_mixed(*it, j0 / BN)) {
+          // Some rows do not see all keys of this tile. Their P is 0 there, but 0 times an infinity or NaN is
+          // NaN: such values (whatever lies behind a sequence's end, say) are taken out of V before the
+          // product, and rows that do see them get them back in the epilogue.
+          span_clean_tile<C, BN>(ctl, smem, wt, slot, grp, quarter * 32 + lane, j0 / BN, entry);
+          __syncwarp();
+        }
         ptx::tc_fence_before();
         ptx::mbar_arrive(BAR(p_full[grp]));
       }
       // ----- epilogue
+      // Adds the non-finite values of the keys that this thread's row sees (in its columns of a tile) to columns
+      // c0 .. c0 + 31 of its sums.
+      auto repair = [&](uint32_t (&rr)[32], int c0) {
+        const int n_bad = *static_cast<volatile int*>(&ctl->info[slot].n_bad);
+        if (n_bad == 0 || !valid) return;
+        int b, n, h;
+        row_of(it, b, n, h);
+        // more tiles than the list holds: all tiles of the item's range
+        const bool listed = n_bad <= kSpanBad;
+        const int last = listed ? n_bad : (ke + BN - 1) / BN;
+        for (int x = listed ? 0 : ks / BN; x < last; ++x) {
+          const int j = listed ? ctl->info[slot].bad[x] : x;
+          const int m0 = max(ks, j * BN + col0), m1 = min(ke, j * BN + col0 + NC);
+          for (int m = m0; m < m1; ++m) {
+            const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + b * p.v_stride[0] + m * p.v_stride[1] +
+                                                                  it->hk * p.v_stride[2] + c0);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) {
+              const uint32_t w = __ldg(v + y);
+              if ((w & 0x7f80u) == 0x7f80u)
+                rr[2 * y] = __float_as_uint(__uint_as_float(rr[2 * y]) + __uint_as_float(w << 16));
+              if ((w & 0x7f800000u) == 0x7f800000u)
+                rr[2 * y + 1] = __float_as_uint(__uint_as_float(rr[2 * y + 1]) + __uint_as_float(w & 0xffff0000u));
+            }
+          }
+        }
+      };
       if (BIAS && F == 1) ptx::named_bar_sync(gbar, 128);  // the position buffer becomes the staging area
       if (n_live > 0) {
         wt.wait(BAR(pv_done[grp]), pv_phase & 1);
@@ -875,6 +1001,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           uint32_t rr[32];
           ptx::tmem_ld32(o_tmem + c * 32, rr);
           ptx::tmem_wait_ld();
+          repair(rr, c * 32);
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             *reinterpret_cast<uint4*>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) =
@@ -922,6 +1049,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
             uint32_t rr[32];
             ptx::tmem_ld32(o_tmem + c * 32, rr);
             ptx::tmem_wait_ld();
+            repair(rr, c * 32);
             float4* dst = reinterpret_cast<float4*>(part + r * D + c * 32);
             // (a part without keys is not read: its row sum says so)
             if (valid && !empty)
@@ -954,6 +1082,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
             uint32_t rr[32];
             ptx::tmem_ld32(o_tmem + c * 64 + half * 32, rr);
             ptx::tmem_wait_ld();
+            repair(rr, c * 64 + half * 32);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               uint32_t w[4];

@@ -157,3 +157,188 @@ def test_caps_from_saturated_to_idle(d, cap):
     q, k, v = make(11, (1, 150, 2, d), (1, 200, 2, d), (1, 200, 2, d), gain=2.2)
     got = la.lite_attn_span(q, k, v, sp.padded_spans([170], 150), cap=cap)
     check(got, ref.span_attention(f64(q), f64(k), f64(v), f64(sp.padded_spans([170], 150)), cap=cap))
+
+
+def check_special(got, want):
+    """check() where the oracle's values are finite; the same NaN and infinities elsewhere."""
+    o, lse = got
+    ro, rl, rw = want
+    a = f64(o)
+    fine = np.isfinite(ro)
+    assert (np.isfinite(a) == fine).all(), np.argwhere(np.isfinite(a) != fine)[:4]
+    assert (np.isnan(a) == np.isnan(ro)).all() and (a[np.isinf(ro)] == ro[np.isinf(ro)]).all()
+    rw = np.where(fine, rw, 0.0)
+    err = np.abs(np.where(fine, a - ro, 0.0))
+    assert (err <= (2.0 ** -8 + 1e-3) * rw + 2.0 ** -8 * np.abs(np.where(fine, ro, 0.0)) + 1e-30).all()
+    x = f64(lse)
+    ok = np.isfinite(rl)
+    assert (np.isfinite(x) == ok).all() and np.abs(x[ok] - rl[ok]).max() <= 4e-4 + 2.0 ** -20 * np.abs(rl[ok]).max()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 7, 100, 300])
+@pytest.mark.parametrize("kw", [{}, {"cap": 5.0}])
+def test_garbage_behind_the_sequences(d, Nq, kw):
+    # what lies behind a sequence's end in a padded batch is anything: NaN, infinities, huge values
+    B, Nk, H = 3, 700, 2
+    lengths = [700, 333, 1]
+    q, k, v, kp, vp = make(Nq, (B, Nq, H, d), (B, Nk, H, d), (B, Nk, H, d), (140, H, d), (140, H, d))
+    spans = sp.padded_spans(lengths, Nq)
+    want = ref.span_attention(f64(q), f64(k), f64(v), f64(spans), **kw)
+    both = ref.span_attention(f64(q), f64(k), f64(v), f64(spans), f64(kp), f64(vp), **kw)
+    for b, n in enumerate(lengths):
+        k[b, n:] = float("nan")
+        v[b, n:, 0] = float("nan")
+        v[b, n:, 1] = float("-inf")
+        k[b, n + 1 :: 3] = 3e38
+        v[b, n + 2 :: 5] = float("inf")
+    check(la.lite_attn_span(q, k, v, spans, **kw), want)
+    check(la.lite_attn_prefix(q, kp, vp, k, v, spans, **kw), both)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("H,Hk", [(2, 2), (6, 2)])
+def test_values_that_are_not_finite_reach_the_rows_that_see_them_only(d, H, Hk):
+    N = 420
+    q, k, v = make(1, (1, N, H, d), (1, N, Hk, d), (1, N, Hk, d))
+    inf, nan = float("inf"), float("nan")
+    v[0, 3, 0, 5] = inf
+    v[0, 60, 1, 0] = nan
+    v[0, 130, 0, 5] = -inf
+    v[0, 200, 0, 9] = inf
+    v[0, 201, 1, d - 1] = -inf
+    v[0, 410, :, 33] = nan
+    with np.errstate(invalid="ignore"):
+        for spans in (sp.prefix_spans(N, 0), sp.document_spans([50, 100, 20, 250]), sp.frame_spans(21, 20, window=3), None):
+            want = ref.span_attention(f64(q), f64(k), f64(v), f64(spans))
+            check_special(la.lite_attn_span(q, k, v, spans), want)
+        one = sp.padded_spans([205], 3, causal=True)
+        want = ref.span_attention(f64(q[:, :3]), f64(k), f64(v), f64(one))
+        check_special(la.lite_attn_span(q[:, :3].contiguous(), k, v, one), want)
+
+
+def test_not_finite_values_in_more_tiles_than_an_item_lists():
+    N, d = 1500, 64
+    q, k, v = make(4, (1, N, 1, d), (1, N, 1, d), (1, N, 1, d))
+    v[0, 7::97, 0, 3] = float("nan")
+    n = torch.arange(N)
+    spans = torch.stack([(n * 7919) % N, torch.clamp((n * 7919) % N + 40, max=N)], -1).int().cuda()
+    with np.errstate(invalid="ignore"):
+        check_special(la.lite_attn_span(q, k, v, spans), ref.span_attention(f64(q), f64(k), f64(v), f64(spans)))
+
+
+def test_strided_views_and_a_batch_that_shares_its_keys():
+    B, N, H, d = 3, 190, 2, 128
+    qkv, kv = make(6, (B, N, 3 * H, d), (1, N, 2 * H, d))
+    q, k, v = qkv[:, :, :H], qkv[:, :, H : 2 * H], qkv[:, :, 2 * H :]
+    check(la.lite_attn_span(q, k, v, sp.prefix_spans(N, 3)),
+          ref.span_attention(f64(q), f64(k), f64(v), f64(sp.prefix_spans(N, 3))))
+    k1, v1 = kv[:, :, :H].expand(B, -1, -1, -1), kv[:, :, H:].expand(B, -1, -1, -1)
+    check(la.lite_attn_span(q, k1, v1), ref.span_attention(f64(q), f64(k1), f64(v1)))
+    q1 = q[:1].expand(B, -1, -1, -1)
+    check(la.lite_attn_prefix(q1[:, :5], kv[0, :, :H], kv[0, :, H:], k, v),
+          ref.span_attention(f64(q1[:, :5]), f64(k), f64(v), None, f64(kv[0, :, :H]), f64(kv[0, :, H:])))
+    # one token a sequence out of a wider buffer: evenly spaced, so it can be stacked
+    check(la.lite_attn_prefix(q[:, :1], kv[0, :, :H], kv[0, :, H:], k, v),
+          ref.span_attention(f64(q[:, :1]), f64(k), f64(v), None, f64(kv[0, :, :H]), f64(kv[0, :, H:])))
+
+
+def test_a_cache_past_32_bit_offsets():
+    Nk, Hk, d = 600_000, 30, 128  # 2.3e9 elements; all but the end is uninitialised memory
+    k = torch.empty((1, Nk, Hk, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    (q,) = make(7, (1, 2, Hk, d))
+    tail = 300
+    k[:, -tail:], v[:, -tail:] = make(8, (1, tail, Hk, d), (1, tail, Hk, d))
+    spans = torch.tensor([[Nk - tail, Nk], [Nk - 17, Nk - 1]], dtype=torch.int32, device="cuda")
+    want = ref.span_attention(f64(q), f64(k[:, -tail:]), f64(v[:, -tail:]), np.array([[0, tail], [tail - 17, tail - 1]]))
+    check(la.lite_attn_span(q, k, v, spans), want)
+    q2 = q.expand(1, 2, Hk, d)
+    k2 = k.as_strided((2, 200, Hk, d), ((Nk - 250) * Hk * d, Hk * d, d, 1))  # a batch stride past 2^31
+    k2[0], k2[1] = make(9, (200, Hk, d), (200, Hk, d))
+    q2 = torch.cat([q, q])
+    check(la.lite_attn_span(q2, k2, k2), ref.span_attention(f64(q2), f64(k2), f64(k2)))
+
+
+def test_equal_calls_give_equal_bits_on_any_grid():
+    lengths = [1, 700, 3, 256, 11, 129, 300, 2]
+    N = sum(lengths)
+    q, k, v = make(10, (2, N, 4, 128), (2, N, 4, 128), (2, N, 4, 128))
+    spans = sp.document_spans(lengths)
+    (q1,) = make(12, (2, 1, 4, 128))
+    first = la.lite_attn_span(q, k, v, spans), la.lite_attn_span(q1, k, v)
+    try:
+        for ctas in (0, 1, 7):
+            la.lite_set_option(la.LITE_OPT_MAX_CTAS, ctas)
+            again = la.lite_attn_span(q, k, v, spans), la.lite_attn_span(q1, k, v)
+            for a, b in zip(first, again):
+                assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    finally:
+        la.lite_set_option(la.LITE_OPT_MAX_CTAS, 0)
+
+
+def _calls():
+    """Calls of each kind with their inputs: split and joined, stacked, handed out by a counter, direct."""
+    q, k, v, kp, vp = make(20, (4, 1, 5, 128), (4, 900, 5, 128), (4, 900, 5, 128), (2000, 5, 128), (2000, 5, 128))
+    big = make(21, (1, 2600, 24, 64), (1, 2600, 24, 64), (1, 2600, 24, 64))
+    docs = sp.document_spans([1000, 7, 1593])
+    ragged = sp.padded_spans([900, 3, 451, 0], 1)
+    return [
+        lambda **kw: la.lite_attn_span(q, k, v, ragged, **kw),
+        lambda **kw: la.lite_attn_prefix(q, kp, vp, k, v, **kw),
+        lambda **kw: la.lite_attn_span(*big, docs, cap=10.0, **kw),
+    ]
+
+
+def test_captured_and_replayed_beside_an_eager_call():
+    for call in _calls():
+        want = call()
+        o, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+        torch.cuda.synchronize()
+        g, h = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        o2, lse2 = torch.zeros_like(o), torch.zeros_like(lse)
+        with torch.cuda.graph(g):
+            call(o=o, lse=lse)
+        with torch.cuda.graph(h):
+            call(o=o2, lse=lse2)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            o.zero_(), lse.zero_()
+            g.replay()
+            with torch.cuda.stream(s):
+                h.replay()
+            eager = call()
+            torch.cuda.synchronize()
+            for a, b in ((o, lse), (o2, lse2), eager):
+                assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+def test_two_streams_at_once():
+    for call in _calls():
+        want = call()
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in range(3)]
+        got = [call(stream=s) for s in streams for _ in range(3)]
+        torch.cuda.synchronize()
+        for a, b in got:
+            assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+def test_a_stalled_kernel_gives_up_and_says_so():
+    q, k, v = make(30, (1, 300, 2, 128), (1, 300, 2, 128), (1, 300, 2, 128))
+    (q1,) = make(31, (1, 1, 2, 128))
+    want = la.lite_attn_span(q, k, v), la.lite_attn_span(q1, k, v)
+    assert la.lite_get_device_status() == 0
+    la.lite_set_option(la.LITE_OPT_WAIT_LIMIT_NS, 2_000_000)
+    la.lite_set_option(la.LITE_OPT_DEBUG_STALL, 1)
+    try:
+        for x in (q, q1):
+            la.lite_attn_span(x, k, v)
+            assert la.lite_get_device_status() == la.LITE_ERR_TIMEOUT
+    finally:
+        la.lite_set_option(la.LITE_OPT_DEBUG_STALL, 0)
+        la.lite_set_option(la.LITE_OPT_WAIT_LIMIT_NS, 4_000_000_000)
+    for x, w in zip((q, q1), want):
+        got = la.lite_attn_span(x, k, v)
+        assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
