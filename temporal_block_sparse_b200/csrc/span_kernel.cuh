@@ -107,7 +107,6 @@ struct SpanTile {
   int n_live, n_pre;
   int j_first;
   int q0, step;
-  int full_lo, full_hi;  // every row sees the own keys [full_lo, full_hi)
 };
 
 struct SpanInfo {
@@ -117,15 +116,11 @@ struct SpanInfo {
   int slot;              // index of its first part in scratch
   int v_first;
   uint32_t u0;           // union index of its first tile
-  int clean0, clean1;    // every row sees all keys of the own tiles [clean0, clean1)
+  int full_lo, full_hi;  // every row of both tiles sees the own keys [full_lo, full_hi)
   int n_bad;             // own key tiles whose non-finite values were taken out of shared memory (see
   int bad[kSpanBad];     // span_clean), the first kSpanBad of them by index
   SpanTile t[2];
 };
-
-// Whether some row of the item may not see all keys of own key tile j (the same answer for both groups and the
-// producer; a tile that only one query tile computes may be counted for the other's sake).
-__device__ __forceinline__ bool span_mixed(const SpanInfo& it, int j) { return j < it.clean0 || j >= it.clean1; }
 
 // Place of own key tile j (entry q of its list) among the item's union tiles.
 __device__ __forceinline__ int span_union(const SpanInfo& it, int j, int q) {
@@ -166,6 +161,7 @@ struct alignas(8) SpanCtl {
   uint64_t kv_full[2], kv_free[2];
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t item_full[2], item_empty[2];
+  uint64_t cleaned;      // both groups have cleaned their halves of a V tile
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -213,7 +209,7 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
   const int ntok = prefix ? p.B * p.Nq : p.Nq;
   const int tp = (prefix || p.fused) ? p.Tp : 0;
   int jlo = 0x7fffffff, jhi = 0;  // own key tiles that either query tile has to see
-  int tlo[2], thi[2];             // and each of them
+  int tlo[2] = {0, 0}, thi[2] = {0, 0}, full_lo[2] = {0, 0}, full_hi[2] = {p.Nk, p.Nk};  // and each of them
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     SpanTile& t = it.t[g];
@@ -227,8 +223,6 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
     const int toks = max(0, min(ps.TN, ntok - t.tok0));
     t.rows = toks * p.G;
     tlo[g] = thi[g] = 0;
-    t.full_lo = 0;
-    t.full_hi = p.Nk;
     if (it.kind == 0 && toks > 0) {
       int lo = 0x7fffffff, hi = 0, flo = 0, fhi = p.Nk;
       if (p.spans) {
@@ -256,20 +250,19 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
         jlo = min(jlo, tlo[g]);
         jhi = max(jhi, thi[g]);
       }
-      t.full_lo = flo;
-      t.full_hi = fhi;
+      full_lo[g] = flo;
+      full_hi[g] = fhi;
     }
   }
   if (jhi == 0) jlo = 0;
-  int clo = 0, chi = p.Nk;
+  it.full_lo = 0;
+  it.full_hi = p.Nk;
 #pragma unroll
   for (int g = 0; g < 2; ++g)
     if (thi[g] > tlo[g]) {
-      clo = max(clo, it.t[g].full_lo);
-      chi = min(chi, it.t[g].full_hi);
+      it.full_lo = max(it.full_lo, full_lo[g]);
+      it.full_hi = min(it.full_hi, full_hi[g]);
     }
-  it.clean0 = clo / BN + (clo % BN != 0);
-  it.clean1 = chi == p.Nk ? 0x7fffffff : chi / BN;
   // virtual tiles: prefix [0, tp), then own jlo .. jhi; this split's are [v0, v1)
   const long long total = tp + (jhi - jlo);
   const int v0 = int(total * split / ps.splits), v1 = int(total * (split + 1) / ps.splits);
@@ -288,9 +281,9 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
 }
 
 // This thread's part in cleaning own key tile j (entry q of its group's list): both groups have a half of it each
-// when both compute it.
+// when both compute it, and then true, for neither may have its product before both are done.
 template <typename C, int BN>
-__device__ __noinline__ void span_clean_tile(SpanCtl* ctl, uint8_t* smem, const Waiter& wt, int slot, int grp, int tid,
+__device__ __noinline__ bool span_clean_tile(SpanCtl* ctl, uint8_t* smem, const Waiter& wt, int slot, int grp, int tid,
                                              int j, int q) {
   SpanInfo& it = ctl->info[slot];
   const uint32_t u = it.u0 + span_union(it, j, q);
@@ -299,16 +292,17 @@ __device__ __noinline__ void span_clean_tile(SpanCtl* ctl, uint8_t* smem, const 
   wt.wait(ptx::smem_addr(&ctl->kv_full[(u + 1) & 1]), ((u + 1) >> 1) & 1);  // V_u comes with bundle u + 1
   if (!span_clean(smem + C::OFF_V + (u & 1) * C::KV_BYTES, both ? grp * 128 + tid : tid, both ? 256 : 128,
                   C::KV_BYTES / 16))
-    return;
+    return both;
   ptx::fence_proxy_async_smem();
   for (int x = 0; x < kSpanBad; ++x) {
     const int old = atomicCAS(&it.bad[x], -1, j);
     if (old == -1 || old == j) {
       atomicMax(&it.n_bad, x + 1);
-      return;
+      return both;
     }
   }
   atomicMax(&it.n_bad, kSpanBad + 1);
+  return both;
 }
 
 // Shared memory: lite_attn_kernel's layout, with a staging area of 32 rows x 128 bytes a softmax warp.
@@ -324,7 +318,6 @@ struct SpanCfg : AttnCfg<D, BN> {
 };
 
 constexpr uint32_t kSpanAlt = 2048u;    // ring word: both groups use the first query tile
-constexpr uint32_t kSpanCheck = 4096u;  // V may be cleaned by either group before any of its products
 
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
@@ -336,14 +329,188 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 
+// PC (16 or 32) score columns of this lane's row, not yet waited for
+template <int PC>
+__device__ __forceinline__ void span_load(uint32_t at, float (&v)[PC]) {
+  if constexpr (PC == 32)
+    ptx::tmem_ld32(at, reinterpret_cast<uint32_t(&)[32]>(v));
+  else
+    tmem_ld16(at, reinterpret_cast<uint32_t(&)[16]>(v));
+}
+
+// four running maxima over the columns, and their maximum
+template <int PC>
+__device__ __forceinline__ void span_max(const float (&v)[PC], float (&m)[4]) {
+#pragma unroll
+  for (int x = 0; x < PC; x += 8) {
+    m[0] = ptx::fmax3(m[0], v[x], v[x + 1]);
+    m[1] = ptx::fmax3(m[1], v[x + 2], v[x + 3]);
+    m[2] = ptx::fmax3(m[2], v[x + 4], v[x + 5]);
+    m[3] = ptx::fmax3(m[3], v[x + 6], v[x + 7]);
+  }
+}
+__device__ __forceinline__ float span_max4(const float (&m)[4]) { return ptx::fmax3(m[0], m[1], fmaxf(m[2], m[3])); }
+
+// P = 2^exponent of PC columns, in bf16 to TMEM (over score columns that have been read) and summed in acc;
+// exponent(x) gives columns x, x + 1
+template <int PC, typename E>
+__device__ __forceinline__ void span_put(uint32_t at, float2 (&acc)[4], E exponent) {
+  uint32_t pk[PC / 2];
+#pragma unroll
+  for (int x = 0; x < PC / 2; ++x) {
+    const float2 a = exponent(2 * x);
+    const float2 pp = make_float2(ptx::ex2(a.x), ptx::ex2(a.y));
+    acc[x & 3] = __fadd2_rn(acc[x & 3], pp);
+    const __nv_bfloat162 h2 = __floats2bfloat162_rn(pp.x, pp.y);
+    pk[x] = *reinterpret_cast<const uint32_t*>(&h2);
+  }
+  if constexpr (PC == 32)
+    ptx::tmem_st16(at, pk);
+  else
+    ptx::tmem_st8(at, pk);
+}
+
+// F = 4: the other quarters' key columns of the row are another lane's, P = 0 there
+template <int NC>
+__device__ __forceinline__ void span_zero(uint32_t s_tmem, int quarter) {
+  uint32_t zero[NC / 2];
+#pragma unroll
+  for (int x = 0; x < NC / 2; ++x) zero[x] = 0u;
+#pragma unroll
+  for (int c = 1; c < 4; ++c) {
+    const uint32_t at = s_tmem + ((quarter + c) & 3) * (NC / 2);
+    if constexpr (NC == 32)
+      ptx::tmem_st16(at, zero);
+    else
+      ptx::tmem_st8(at, zero);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void span_rescale(uint32_t o_tmem, float alpha) {
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t rr[32];
+    ptx::tmem_ld32(o_tmem + c * 32, rr);
+    ptx::tmem_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 32; ++x) rr[x] = __float_as_uint(__uint_as_float(rr[x]) * alpha);
+    ptx::tmem_st32(o_tmem + c * 32, rr);
+  }
+}
+
+// A key tile for which the short way does not do (a span ends in it, scores near the cap, rows on both sides of it,
+// given positions): every score of the warp's rows in full, back into TMEM, then the exponentials. Keys
+// [lo, hi) of this thread's NC columns are seen. Takes and returns (reference, row sum).
+// Out of line, for the registers of the tiles that need none of it.
+template <int D, int NC, int MOD, int F>
+__device__ __noinline__ float2 span_tile_in_full(const SpanParams& p, uint32_t s_tmem, uint32_t o_tmem, int quarter,
+                                                 int lo, int hi, float base, float slope, float qp, const float* kpos,
+                                                 float2 ml, bool rescale) {
+  constexpr bool CAP = (MOD & kSpanCap) != 0, BIAS = (MOD & kSpanBias) != 0;
+  constexpr int PC = NC < 32 ? NC : 32;
+  const int col0 = F == 1 ? 0 : quarter * NC;
+  float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  float v[PC];
+#pragma unroll 1
+  for (int c = 0; c < NC / PC; ++c) {
+    span_load<PC>(s_tmem + col0 + c * PC, v);
+    ptx::tmem_wait_ld();
+    // the keys seen among these columns as bits: one select per column
+    const int a = min(max(lo - PC * c, 0), 32), z = min(max(hi - PC * c, 0), 32);
+    const uint32_t upto = z >= 32 ? 0xffffffffu : ((1u << z) - 1u);
+    const uint32_t below = a >= 32 ? 0xffffffffu : ((1u << a) - 1u);
+    const uint32_t bits = upto & ~below;
+    const float at = base + float(PC * c);
+    const float* kc = kpos + PC * c;
+#pragma unroll
+    for (int x = 0; x < PC; ++x) {
+      float t = v[x] * p.scale_log2;
+      if (CAP) {
+        // cap tanh(z) = cap - 2 cap / (1 + e^{2z}), in log2 units; both ends saturate exactly. Near zero it cancels
+        // (a large cap against small scores), and the polynomial takes over.
+        const float y = v[x] * v[x];
+        const float far = fmaf(-2.f * p.cap_c, fast_rcp(1.f + ptx::ex2(v[x] * p.cap_a)), p.cap_c);
+        t = v[x] * fmaf(fmaf(fmaf(fmaf(p.cap_b[4], y, p.cap_b[3]), y, p.cap_b[2]), y, p.cap_b[1]), y, p.cap_b[0]);
+        t = fabsf(v[x]) <= p.cap_mid ? t : far;
+      }
+      if (BIAS) t = fmaf(-slope, fabsf(kpos ? kc[x] - qp : at + float(x)), t);
+      v[x] = (bits & (1u << x)) ? t : -INFINITY;
+    }
+    span_max<PC>(v, m);
+    if constexpr (PC == 32)
+      ptx::tmem_st32(s_tmem + col0 + c * 32, reinterpret_cast<uint32_t(&)[32]>(v));
+    else
+      ptx::tmem_st16(s_tmem + col0, reinterpret_cast<uint32_t(&)[16]>(v));
+  }
+  ptx::tmem_wait_st();
+  const float loc = span_max4(m);
+  float m_used = ml.x, l = ml.y, alpha = 1.f;
+  const bool need = loc > m_used + kRescaleLog2;
+  if (need) {
+    alpha = ptx::ex2(m_used - loc);
+    m_used = loc;
+    l *= alpha;
+  }
+  const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+  const float2 nm2 = make_float2(neg_m, neg_m);
+  float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+  for (int c = 0; c < NC / PC; ++c) {
+    span_load<PC>(s_tmem + col0 + c * PC, v);
+    ptx::tmem_wait_ld();
+    span_put<PC>(s_tmem + col0 / 2 + c * (PC / 2), acc, [&](int x) { return __fadd2_rn(make_float2(v[x], v[x + 1]), nm2); });
+  }
+  if constexpr (F > 1) span_zero<NC>(s_tmem, quarter);
+  if (__any_sync(0xffffffffu, need) && rescale) span_rescale<D>(o_tmem, alpha);
+  ptx::tmem_wait_st();
+  const float2 acc2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+  return make_float2(m_used, l + acc2.x + acc2.y);
+}
+
+// Adds the non-finite values of the keys [ks, ke) that this thread's row sees (columns col0 .. col0 + NC of each
+// tile) to its row of O: those of the tiles that were cleaned for the item.
+template <int D, int BN, int NC>
+__device__ __noinline__ void span_repair(const SpanParams& p, const SpanInfo& it, uint32_t o_tmem, bool valid, int ks,
+                                         int ke, int b, int col0) {
+  // more tiles than the list holds: all tiles of the row's span
+  const bool listed = it.n_bad <= kSpanBad;
+  const int x0 = listed ? 0 : ks / BN, x1 = listed ? it.n_bad : (ke + BN - 1) / BN;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint32_t rr[32];
+    ptx::tmem_ld32(o_tmem + c * 32, rr);
+    ptx::tmem_wait_ld();
+    for (int x = x0; valid && x < x1; ++x) {
+      const int j = listed ? it.bad[x] : x;
+      const int m1 = min(ke, j * BN + col0 + NC);
+      for (int m = max(ks, j * BN + col0); m < m1; ++m) {
+        const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + b * p.v_stride[0] + m * p.v_stride[1] +
+                                                              it.hk * p.v_stride[2] + c * 32);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const uint32_t w = __ldg(v + y);
+          if ((w & 0x7f80u) == 0x7f80u) rr[2 * y] = __float_as_uint(__uint_as_float(rr[2 * y]) + __uint_as_float(w << 16));
+          if ((w & 0x7f800000u) == 0x7f800000u)
+            rr[2 * y + 1] = __float_as_uint(__uint_as_float(rr[2 * y + 1]) + __uint_as_float(w & 0xffff0000u));
+        }
+      }
+    }
+    __syncwarp();
+    ptx::tmem_st32(o_tmem + c * 32, rr);
+    ptx::tmem_wait_st();
+  }
+}
+
 template <int D, int BN, int MOD, int F>
 __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
     lite_span_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmQp,
                      const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                      const __grid_constant__ CUtensorMap tmKp, const __grid_constant__ CUtensorMap tmVp,
-                     const SpanParams p) {
+                     const __grid_constant__ SpanParams p) {
   using C = SpanCfg<D, BN>;
   constexpr int NC = BN / F;  // key columns of a thread
+  constexpr int PC = NC < 32 ? NC : 32;  // loaded, converted and stored at a time
   constexpr bool CAP = (MOD & kSpanCap) != 0, BIAS = (MOD & kSpanBias) != 0;
   static_assert(sizeof(SpanCtl) <= C::CTL_BYTES, "control block");
   // key positions of two tiles per warpgroup share the group's staging area
@@ -372,6 +539,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       ptx::mbar_init(BAR(item_full[b]), 1);
       ptx::mbar_init(BAR(item_empty[b]), 8);
     }
+    ptx::mbar_init(BAR(cleaned), 256);
     ptx::mbar_init(BAR(drain), 1);
     ctl->abort = 0;
     ptx::fence_mbar_init();
@@ -498,7 +666,6 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
                 ++d1;
               }
               if (d0 == n0 && d1 == n1) f |= kItemLast;
-              if (!pre && span_mixed(it, j)) f |= kSpanCheck;
               ok = bundle(true, pre, j, it.hk, it.b, f);
               f = 0u;
             }
@@ -575,13 +742,6 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           ptx::mma_commit(BAR(s_full[g]));
           return true;
         };
-        if (prev & kSpanCheck) {
-          // either group may still be cleaning V: both have to be done with the tile
-#pragma unroll
-          for (int g = 0; g < 2; ++g)
-            if (ok && (prev & (kLive0 << g))) ok = wt.wait(BAR(p_full[g]), pc[g] & 1);
-          if (!ok) break;
-        }
         if (prev & f & (kLive0 | kLive1)) {
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
@@ -633,7 +793,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       }
       h = it->hk * p.G + r_head;
     };
-    uint32_t tg = 0, items = 0, pv_phase = 0;
+    uint32_t tg = 0, items = 0, pv_phase = 0, cleaned = 0;
     while (true) {
       const int slot = items & 1;
       bool ok = wt.wait(BAR(item_full[slot]), (items >> 1) & 1);
@@ -682,117 +842,45 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           ptx::named_bar_sync(gbar, 128);
         }
         if (BIAS && idx + 1 < n_live) kp_next = key_pos(idx + 1);
+        const bool masked = pre ? p.Np - j0 < BN : (it->full_lo > j0 || it->full_hi < j0 + BN);
         wt.wait(BAR(s_full[grp]), tg & 1);
         ++tg;
         __syncwarp();
         ptx::tc_fence_after();
         if (warp_valid) {
-          constexpr int PC = NC < 32 ? NC : 32;  // columns loaded, converted and stored at a time
-          const auto load_scores = [&](int c, float (&v)[PC]) {
-            if constexpr (PC == 32)
-              ptx::tmem_ld32(s_tmem + col0 + c * 32, reinterpret_cast<uint32_t(&)[32]>(v));
-            else
-              tmem_ld16(s_tmem + col0, reinterpret_cast<uint32_t(&)[16]>(v));
-          };
-          // columns [lo, hi) of the tile are keys that this row sees
-          const int lo = pre ? 0 : ks - j0, hi = pre ? p.Np - j0 : ke - j0;
-          const bool masked = pre ? hi < BN : (mt->full_lo > j0 || mt->full_hi < j0 + BN);
-          // the keys seen among columns col0 + 32 c and on, as bits: one select per column then
-          const auto seen = [&](int c) -> uint32_t {
-            const int at = col0 + 32 * c;
-            const int a = min(max(lo - at, 0), 32), z = min(max(hi - at, 0), 32);
-            const uint32_t upto = z >= 32 ? 0xffffffffu : ((1u << z) - 1u);
-            const uint32_t below = a >= 32 ? 0xffffffffu : ((1u << a) - 1u);
-            return upto & ~below;
-          };
-          const auto row_max = [](const auto& v, int n, float (&m)[4]) {
-#pragma unroll
-            for (int x = 0; x < n; x += 8) {
-              m[0] = ptx::fmax3(m[0], v[x], v[x + 1]);
-              m[1] = ptx::fmax3(m[1], v[x + 2], v[x + 3]);
-              m[2] = ptx::fmax3(m[2], v[x + 4], v[x + 5]);
-              m[3] = ptx::fmax3(m[3], v[x + 6], v[x + 7]);
-            }
-          };
-          const auto all4 = [](const float (&m)[4]) { return ptx::fmax3(m[0], m[1], fmaxf(m[2], m[3])); };
+          // Key x of the tile (default positions) is at distance |base + x|; where all rows of the warp have the
+          // tile on one side, the bias is linear in x: sg * (base + x).
+          const float base = BIAS ? float(j0 + col0 + (pre ? 0 : p.Np)) - qp : 0.f;
+          const float sg = base < 0.f ? slope : -slope;
+          bool fast = !masked && !given;
+          if (BIAS)
+            fast = fast && __all_sync(0xffffffffu, !valid || ((base >= 0.f || base <= 1.f - NC) &&
+                                                               fabsf(slope) * PC <= (CAP ? 30.f : 60.f)));
           float loc = -INFINITY;  // the tile's row maximum, or a reference near it (log2 units)
-          // lazy rescale of the accumulator, as in lite_attn_kernel
-          bool need = false;
-          float alpha = 1.f;
-          const auto take_reference = [&]() {
-            need = loc > m_used + kRescaleLog2;
-            if (need) {
-              alpha = ptx::ex2(m_used - loc);
-              m_used = loc;
-              l *= alpha;
-            }
-            // a row that has seen no key yet keeps m_used = -inf; its exponents are -inf - 0
-            return m_used == -INFINITY ? 0.f : -m_used;
-          };
-          float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          // P = 2^(exponent) of chunk c's column pairs, in bf16 over S columns that have been read
-          const auto put_p = [&](int c, auto exponent) {
-            uint32_t pk[PC / 2];
-#pragma unroll
-            for (int x = 0; x < PC / 2; ++x) {
-              const float2 a = exponent(2 * x);
-              const float2 pp = make_float2(ptx::ex2(a.x), ptx::ex2(a.y));
-              acc[x & 3] = __fadd2_rn(acc[x & 3], pp);
-              __nv_bfloat162 h2 = __floats2bfloat162_rn(pp.x, pp.y);
-              pk[x] = *reinterpret_cast<uint32_t*>(&h2);
-            }
-            if constexpr (PC == 32)
-              ptx::tmem_st16(s_tmem + col0 / 2 + c * 16, pk);
-            else
-              ptx::tmem_st8(s_tmem + col0 / 2, pk);
-          };
-          const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-          if constexpr (MOD == 0) {
-            // the row is read once and stays in registers for the maximum and the exponentials
-            float v[NC / PC][PC];
-#pragma unroll
-            for (int c = 0; c < NC / PC; ++c) load_scores(c, v[c]);
-            ptx::tmem_wait_ld();
-            if (masked) {
-#pragma unroll
-              for (int c = 0; c < NC / PC; ++c) {
-                const uint32_t bits = seen(c);
-#pragma unroll
-                for (int x = 0; x < PC; ++x) v[c][x] = (bits & (1u << x)) ? v[c][x] : -INFINITY;
-              }
-            }
-            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int c = 0; c < NC / PC; ++c) row_max(v[c], PC, m);
-            loc = all4(m) * p.scale_log2;
-            const float neg_m = take_reference();
-            const float2 nm2 = make_float2(neg_m, neg_m);
-#pragma unroll
-            for (int c = 0; c < NC / PC; ++c)
-              put_p(c, [&](int x) { return __ffma2_rn(make_float2(v[c][x], v[c][x + 1]), sc2, nm2); });
-          } else {
-            // Key x of the tile (default positions) is at distance |base + x|; where all rows of the warp have
-            // the tile on one side, the bias is linear in x: sg * (base + x).
-            const float base = BIAS ? float(j0 + col0 + (pre ? 0 : p.Np)) - qp : 0.f;
-            const float sg = base < 0.f ? slope : -slope;
+          float v[MOD == 0 ? NC / PC : 2][PC];
+          if (fast) {
             // The exponents of a row need a reference near its maximum, not the maximum: P has the same
-            // relative precision at every scale. Here it is at most 2 * 24 + 30 above (the largest |score|
-            // taken for the score under a cap, the bias's spread over 32 columns; 60 without a cap), and 2^-78
-            // is far from the end of the range. So a tile that needs no mask takes it from the raw scores, and the cap and the bias
-            // are packed products inside the exponent. The scores are read from TMEM twice, 32 at a time: a
-            // whole row in registers left too few of them to keep these longer chains apart.
-            bool fast = !masked && !given;
-            if (BIAS)
-              fast = fast && __all_sync(0xffffffffu, !valid || ((base >= 0.f || base <= 1.f - NC) &&
-                                                                 fabsf(slope) * PC <= (CAP ? 30.f : 60.f)));
-            float v[2][PC];
-            if (fast) {
+            // relative precision at every scale. With a cap or a bias it is at most 2 * 24 + 30 above (the
+            // largest |score| taken for the score under a cap, the bias's spread over 32 columns; 60
+            // without a cap), and 2^-78 is far from the end of the range. So it comes from the raw scores, and
+            // the cap and the bias are packed products inside the exponent. The scores are read from
+            // TMEM twice then, 32 at a time: a whole row in registers leaves too few of them to keep these
+            // longer chains apart. Without cap and bias the row is read once and stays in registers.
+            if constexpr (MOD == 0) {
+#pragma unroll
+              for (int c = 0; c < NC / PC; ++c) span_load<PC>(s_tmem + col0 + c * PC, v[c]);
+              ptx::tmem_wait_ld();
+              float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int c = 0; c < NC / PC; ++c) span_max<PC>(v[c], m);
+              loc = span_max4(m) * p.scale_log2;
+            } else {
               float top = -INFINITY;
-              load_scores(0, v[0]);
+              span_load<PC>(s_tmem + col0, v[0]);
 #pragma unroll
               for (int c = 0; c < NC / PC; ++c) {
                 ptx::tmem_wait_ld();
-                if (c + 1 < NC / PC) load_scores(c + 1, v[(c + 1) & 1]);
+                if (c + 1 < NC / PC) span_load<PC>(s_tmem + col0 + (c + 1) * PC, v[(c + 1) & 1]);
                 float m[4];
                 if constexpr (CAP) {
 #pragma unroll
@@ -802,9 +890,9 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
                 } else {
 #pragma unroll
                   for (int x = 0; x < 4; ++x) m[x] = -INFINITY;
-                  row_max(v[c & 1], PC, m);
+                  span_max<PC>(v[c & 1], m);
                 }
-                const float here = all4(m);
+                const float here = span_max4(m);
                 top = fmaxf(top, here);
                 // (the cap only lowers a score; the bias is largest at one end of the chunk)
                 if (BIAS)
@@ -813,158 +901,97 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
               if (CAP) fast = !__any_sync(0xffffffffu, valid && !(top <= p.cap_near));
               if (!BIAS) loc = top * p.scale_log2;
             }
-            if (fast) {
-              const float neg_m = take_reference();
-              // bias minus reference of columns 2y, 2y + 1 of each eight, stepped from one eight to the next
-              // (at most 16 sums: off by 2^-20 of an exponent that matters)
-              float2 w[4];
-              const float c0 = fmaf(sg, base, neg_m);
+          }
+          if (fast) {
+            // lazy rescale of the accumulator, as in lite_attn_kernel
+            const bool need = loc > m_used + kRescaleLog2;
+            float alpha = 1.f;
+            if (need) {
+              alpha = ptx::ex2(m_used - loc);
+              m_used = loc;
+              l *= alpha;
+            }
+            // a row that has seen no key yet keeps m_used = -inf; its exponents are -inf - 0
+            const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+            const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+            float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            // bias minus reference of columns 2y, 2y + 1 of each eight, stepped from one eight to the next (at
+            // most 16 sums: off by 2^-20 of an exponent that matters)
+            float2 w[4];
+            const float c0 = fmaf(sg, base, neg_m);
 #pragma unroll
-              for (int y = 0; y < 4; ++y)
-                w[y] = BIAS ? make_float2(fmaf(sg, float(2 * y), c0), fmaf(sg, float(2 * y + 1), c0))
-                            : make_float2(neg_m, neg_m);
-              const float2 sg8 = make_float2(8.f * sg, 8.f * sg);
-              load_scores(0, v[0]);
+            for (int y = 0; y < 4; ++y)
+              w[y] = BIAS ? make_float2(fmaf(sg, float(2 * y), c0), fmaf(sg, float(2 * y + 1), c0))
+                          : make_float2(neg_m, neg_m);
+            const float2 sg8 = make_float2(8.f * sg, 8.f * sg);
+            if constexpr (MOD != 0) span_load<PC>(s_tmem + col0, v[0]);
 #pragma unroll
-              for (int c = 0; c < NC / PC; ++c) {
+            for (int c = 0; c < NC / PC; ++c) {
+              if constexpr (MOD != 0) {
                 ptx::tmem_wait_ld();
-                if (c + 1 < NC / PC) load_scores(c + 1, v[(c + 1) & 1]);
-                put_p(c, [&](int x) {
-                  const float2 a = make_float2(v[c & 1][x], v[c & 1][x + 1]);
-                  float2& wx = w[(x >> 1) & 3];
-                  const float2 add = wx;
-                  if (BIAS) wx = __fadd2_rn(wx, sg8);
-                  if constexpr (CAP) {
-                    // cap tanh(s scale / cap) as an odd polynomial: two exponential-unit operations a score
-                    // more would triple the work of the unit that bounds the kernel
-                    const float2 y = __fmul2_rn(a, a);
-                    float2 t = __ffma2_rn(make_float2(p.cap_b[4], p.cap_b[4]), y, make_float2(p.cap_b[3], p.cap_b[3]));
-                    t = __ffma2_rn(t, y, make_float2(p.cap_b[2], p.cap_b[2]));
-                    t = __ffma2_rn(t, y, make_float2(p.cap_b[1], p.cap_b[1]));
-                    t = __ffma2_rn(t, y, make_float2(p.cap_b[0], p.cap_b[0]));
-                    return __ffma2_rn(a, t, add);
-                  } else {
-                    return __ffma2_rn(a, sc2, add);
-                  }
-                });
+                if (c + 1 < NC / PC) span_load<PC>(s_tmem + col0 + (c + 1) * PC, v[(c + 1) & 1]);
               }
-            } else {
-              // Tiles that a span ends in, scores near the cap, tiles on both sides of their rows, given
-              // positions: every score in full, back into TMEM, then the exponentials.
-              loc = -INFINITY;
-              float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-              for (int c = 0; c < NC / PC; ++c) {
-                load_scores(c, v[0]);
-                ptx::tmem_wait_ld();
-                const uint32_t bits = seen(c);
-                const float at = base + float(32 * c);
-                const float* kc = kp + col0 + 32 * c;
-#pragma unroll
-                for (int x = 0; x < PC; ++x) {
-                  float t = v[0][x] * p.scale_log2;
-                  if (CAP) {
-                    // cap tanh(z) = cap - 2 cap / (1 + e^{2z}), in log2 units; both ends saturate exactly.
-                    // Near zero it cancels (a large cap against small scores), and the polynomial takes over.
-                    const float y = v[0][x] * v[0][x];
-                    const float far = fmaf(-2.f * p.cap_c, fast_rcp(1.f + ptx::ex2(v[0][x] * p.cap_a)), p.cap_c);
-                    t = v[0][x] * fmaf(fmaf(fmaf(fmaf(p.cap_b[4], y, p.cap_b[3]), y, p.cap_b[2]), y, p.cap_b[1]), y, p.cap_b[0]);
-                    t = fabsf(v[0][x]) <= p.cap_mid ? t : far;
-                  }
-                  if (BIAS) t = fmaf(-slope, fabsf(given ? kc[x] - qp : at + float(x)), t);
-                  v[0][x] = (!masked || (bits & (1u << x))) ? t : -INFINITY;
+              const float(&vc)[PC] = v[MOD == 0 ? c : (c & 1)];
+              span_put<PC>(s_tmem + col0 / 2 + c * (PC / 2), acc, [&](int x) {
+                const float2 a = make_float2(vc[x], vc[x + 1]);
+                float2& wx = w[(x >> 1) & 3];
+                const float2 add = wx;
+                if (BIAS) wx = __fadd2_rn(wx, sg8);
+                if constexpr (CAP) {
+                  // cap tanh(s scale / cap) as an odd polynomial: two exponential-unit operations a score
+                  // more would triple the work of the unit that bounds the kernel
+                  const float2 y = __fmul2_rn(a, a);
+                  float2 t = __ffma2_rn(make_float2(p.cap_b[4], p.cap_b[4]), y, make_float2(p.cap_b[3], p.cap_b[3]));
+                  t = __ffma2_rn(t, y, make_float2(p.cap_b[2], p.cap_b[2]));
+                  t = __ffma2_rn(t, y, make_float2(p.cap_b[1], p.cap_b[1]));
+                  t = __ffma2_rn(t, y, make_float2(p.cap_b[0], p.cap_b[0]));
+                  return __ffma2_rn(a, t, add);
+                } else {
+                  return __ffma2_rn(a, sc2, add);
                 }
-                row_max(v[0], PC, m);
-                if constexpr (PC == 32)
-                  ptx::tmem_st32(s_tmem + col0 + c * 32, reinterpret_cast<uint32_t(&)[32]>(v[0]));
-                else
-                  ptx::tmem_st16(s_tmem + col0, reinterpret_cast<uint32_t(&)[16]>(v[0]));
-              }
-              ptx::tmem_wait_st();
-              loc = all4(m);
-              const float neg_m = take_reference();
-              const float2 nm2 = make_float2(neg_m, neg_m);
-#pragma unroll 1
-              for (int c = 0; c < NC / PC; ++c) {
-                load_scores(c, v[0]);
-                ptx::tmem_wait_ld();
-                put_p(c, [&](int x) { return __fadd2_rn(make_float2(v[0][x], v[0][x + 1]), nm2); });
-              }
+              });
             }
+            if constexpr (F > 1) span_zero<NC>(s_tmem, quarter);
+            if (__any_sync(0xffffffffu, need) && idx >= 1) span_rescale<D>(o_tmem, alpha);
+            ptx::tmem_wait_st();
+            const float2 acc2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
+            l += acc2.x + acc2.y;
+          } else {
+            // columns [lo, hi) of the tile are keys that this row sees
+            const float2 ml = span_tile_in_full<D, NC, MOD, F>(
+                p, s_tmem, o_tmem, quarter, (pre || !masked) ? 0 : ks - j0 - col0,
+                !masked ? NC : (pre ? p.Np : ke) - j0 - col0, base, slope, qp, given ? kp + col0 : nullptr,
+                make_float2(m_used, l), idx >= 1);
+            m_used = ml.x;
+            l = ml.y;
           }
-          if constexpr (F > 1) {
-            // the other quarters of the row's keys are another lane's: P = 0 there
-            uint32_t zero[NC / 2];
-#pragma unroll
-            for (int x = 0; x < NC / 2; ++x) zero[x] = 0u;
-#pragma unroll
-            for (int c = 1; c < F; ++c) {
-              const uint32_t at = s_tmem + ((quarter + c) & (F - 1)) * (NC / 2);
-              if constexpr (NC == 32)
-                ptx::tmem_st16(at, zero);
-              else
-                ptx::tmem_st8(at, zero);
-            }
-          }
-          if (__any_sync(0xffffffffu, need) && idx >= 1) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t rr[32];
-              ptx::tmem_ld32(o_tmem + c * 32, rr);
-              ptx::tmem_wait_ld();
-#pragma unroll
-              for (int x = 0; x < 32; ++x) rr[x] = __float_as_uint(__uint_as_float(rr[x]) * alpha);
-              ptx::tmem_st32(o_tmem + c * 32, rr);
-            }
-          }
-          ptx::tmem_wait_st();
-          const float2 acc2 = __fadd2_rn(__fadd2_rn(acc[0], acc[1]), __fadd2_rn(acc[2], acc[3]));
-          l += acc2.x + acc2.y;
         }
-        if (!pre && span_mixed(*it, j0 / BN)) {
+        if (masked && !pre && (it->full_lo > j0 || it->full_hi < min(j0 + BN, p.Nk))) {
           // Some rows do not see all keys of this tile. Their P is 0 there, but 0 times an infinity or NaN is
           // NaN: such values (whatever lies behind a sequence's end, say) are taken out of V before the
           // product, and rows that do see them get them back in the epilogue.
-          span_clean_tile<C, BN>(ctl, smem, wt, slot, grp, quarter * 32 + lane, j0 / BN, entry);
+          if (span_clean_tile<C, BN>(ctl, smem, wt, slot, grp, quarter * 32 + lane, j0 / BN, entry)) {
+            ptx::mbar_arrive(BAR(cleaned));
+            wt.wait(BAR(cleaned), cleaned & 1);
+            ++cleaned;
+          }
           __syncwarp();
         }
         ptx::tc_fence_before();
         ptx::mbar_arrive(BAR(p_full[grp]));
       }
       // ----- epilogue
-      // Adds the non-finite values of the keys that this thread's row sees (in its columns of a tile) to columns
-      // c0 .. c0 + 31 of its sums.
-      auto repair = [&](uint32_t (&rr)[32], int c0) {
-        const int n_bad = *static_cast<volatile int*>(&ctl->info[slot].n_bad);
-        if (n_bad == 0 || !valid) return;
-        int b, n, h;
-        row_of(it, b, n, h);
-        // more tiles than the list holds: all tiles of the item's range
-        const bool listed = n_bad <= kSpanBad;
-        const int last = listed ? n_bad : (ke + BN - 1) / BN;
-        for (int x = listed ? 0 : ks / BN; x < last; ++x) {
-          const int j = listed ? ctl->info[slot].bad[x] : x;
-          const int m0 = max(ks, j * BN + col0), m1 = min(ke, j * BN + col0 + NC);
-          for (int m = m0; m < m1; ++m) {
-            const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + b * p.v_stride[0] + m * p.v_stride[1] +
-                                                                  it->hk * p.v_stride[2] + c0);
-#pragma unroll
-            for (int y = 0; y < 16; ++y) {
-              const uint32_t w = __ldg(v + y);
-              if ((w & 0x7f80u) == 0x7f80u)
-                rr[2 * y] = __float_as_uint(__uint_as_float(rr[2 * y]) + __uint_as_float(w << 16));
-              if ((w & 0x7f800000u) == 0x7f800000u)
-                rr[2 * y + 1] = __float_as_uint(__uint_as_float(rr[2 * y + 1]) + __uint_as_float(w & 0xffff0000u));
-            }
-          }
-        }
-      };
       if (BIAS && F == 1) ptx::named_bar_sync(gbar, 128);  // the position buffer becomes the staging area
       if (n_live > 0) {
         wt.wait(BAR(pv_done[grp]), pv_phase & 1);
         ++pv_phase;
         __syncwarp();
         ptx::tc_fence_after();
+        if (warp_valid && *static_cast<volatile const int*>(&it->n_bad) > 0) {
+          int b, n, h;
+          row_of(it, b, n, h);
+          span_repair<D, BN, NC>(p, *it, o_tmem, valid, ks, ke, b, col0);
+        }
       }
       // a row that saw no key: o = 0, lse = -inf (l is 0 then; a NaN score leaves its mark in l)
       const bool empty = l == 0.f;
@@ -1001,7 +1028,6 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           uint32_t rr[32];
           ptx::tmem_ld32(o_tmem + c * 32, rr);
           ptx::tmem_wait_ld();
-          repair(rr, c * 32);
 #pragma unroll
           for (int x = 0; x < 8; ++x)
             *reinterpret_cast<uint4*>(stage + lane * 128 + ((x ^ (lane & 7)) << 4)) =
@@ -1049,8 +1075,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
             uint32_t rr[32];
             ptx::tmem_ld32(o_tmem + c * 32, rr);
             ptx::tmem_wait_ld();
-            repair(rr, c * 32);
-            float4* dst = reinterpret_cast<float4*>(part + r * D + c * 32);
+              float4* dst = reinterpret_cast<float4*>(part + r * D + c * 32);
             // (a part without keys is not read: its row sum says so)
             if (valid && !empty)
 #pragma unroll
@@ -1082,7 +1107,6 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
             uint32_t rr[32];
             ptx::tmem_ld32(o_tmem + c * 64 + half * 32, rr);
             ptx::tmem_wait_ld();
-            repair(rr, c * 64 + half * 32);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               uint32_t w[4];
