@@ -432,9 +432,9 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream);
  *   s = scale q.k;  s <- cap tanh(s / cap) when cap > 0;
  *   s <- s - slopes[h] |q_pos[n] - k_pos[m]| when slopes is given;  o = softmax(s) v,
  *   lse = ln sum exp(s).
- * Query head h uses key head h / (H / Hk). Key tiles that no row of a query tile sees are not loaded;
- * keys outside a row's span do not reach its result, whatever k holds there, and v must be finite
- * in keys that share a 64- or 128-key tile with keys of the row's span.
+ * Query head h uses key head h / (H / Hk). Key tiles that no row of a query tile sees are not loaded.
+ * Keys outside a row's span do not reach its result, whatever k and v hold there (NaN and infinities
+ * included); a value of v that is not finite makes its column of the rows that see it not finite.
  *
  *  q          in   device bf16 [B, Nq, H, d]; k, v in device bf16 [B, Nk, Hk, d]; strides in elements
  *                  (batch, token, head; the head dim is contiguous), positive multiples of 8. A batch

@@ -8,6 +8,11 @@ video; must_do_list / must_skip_list key ranges; return_softmax_lse for combinin
 attentions; SeqParallelLiteAttention(num_nodes, ...) called with the index of the K/V split it
 processes, one skip state per split.
 
+AxisRope holds what a layer does to q and k before its attention (norm weights, rotary axes); a
+LiteAttention that is given one takes the projection's q and k as they are. ChunkedAttention
+generates a video frame by frame: each call's frames attend to a shared history, to the frames
+before them (kept in its key and value cache) and to themselves.
+
 Host bookkeeping only: every tensor operation runs in the CUDA library through lite_attn. The
 state is a pair of mask buffers per (split, shape); each call reads one and writes the other (the
 library copies mask_in into mask_out and ORs new flags), then the pair swaps.
@@ -20,6 +25,7 @@ from typing import Callable, Dict, List, Optional, Sequence, Tuple
 import torch
 
 from . import lite_attn as la
+from .spans import frame_spans
 
 
 class _SkipState:
@@ -56,17 +62,42 @@ class _SkipState:
         return float(bits.flatten(-2)[..., :Tk].float().mean())
 
 
+class AxisRope:
+    """RMS norm and rotary positions of one layer's queries and keys (lite_qk_rope).
+
+    dims: dimensions of the head that each position axis turns (frame, row, column: workload.axis_split).
+    grid: sizes of the token grid, one per axis, last axis fastest; `start` of a call is the grid index of
+    its first token. q_weight, k_weight: fp32 norm weights of d elements (each head by itself) or of
+    heads * d (the token's whole row), or None.
+    """
+
+    def __init__(self, dims: Sequence[int], grid: Sequence[int], theta: float = 10000.0, pairing: str = "interleaved",
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6):
+        self.plan = la.RopePlan(dims, theta=theta, pairing=pairing)
+        self.grid = tuple(int(x) for x in grid)
+        self.q_weight, self.k_weight, self.eps = q_weight, k_weight, float(eps)
+
+    def __call__(self, q: torch.Tensor, k: torch.Tensor, start: int = 0, k_out: Optional[torch.Tensor] = None):
+        """(q, k) normed and turned, bf16, for q [B, N, H, d], k [B, N, Hk, d] in bf16, fp16 or fp32 (strided
+        views are fine); k goes to k_out where given."""
+        return la.lite_qk_rope(q, k, self.plan, grid=self.grid, start=start, q_weight=self.q_weight,
+                               k_weight=self.k_weight, eps=self.eps, k_out=k_out)
+
+
 class LiteAttention:
     """One attention layer's LiteAttention: call it at every denoising step with that step's q, k, v.
 
     threshold: QK-Skip tau (natural-log units of scale * QK^T; README default -10).
     enable_skipping: False computes every tile and neither reads nor updates the skip state.
+    rope: an AxisRope that every call's q and k go through first (None: they come ready).
     """
 
-    def __init__(self, enable_skipping: bool = True, threshold: float = -10.0, max_batch_size: int = 4):
+    def __init__(self, enable_skipping: bool = True, threshold: float = -10.0, max_batch_size: int = 4,
+                 rope: Optional[AxisRope] = None):
         self.enable_skipping = bool(enable_skipping)
         self.threshold = float(threshold)
         self.max_batch_size = int(max_batch_size)
+        self.rope = rope
         self._state = _SkipState()
 
     def enable_skip_optimization(self, enable: bool = True):
@@ -86,6 +117,8 @@ class LiteAttention:
         B, Nq, H, d = q.shape
         if B > self.max_batch_size:
             raise ValueError(f"batch {B} exceeds max_batch_size {self.max_batch_size}")
+        if self.rope is not None:
+            q, k = self.rope(q, k)
         Nk = k.shape[1]
         if not self.enable_skipping:
             if must_do_list or must_skip_list:
@@ -134,6 +167,85 @@ class SeqParallelLiteAttention(LiteAttention):
         if not 0 <= split_idx < self.num_nodes:
             raise IndexError(f"split_idx {split_idx} outside [0, {self.num_nodes})")
         return self._run(self._states[split_idx], q, k, v, scale, return_softmax_lse, must_do_list, must_skip_list)
+
+
+class ChunkedAttention:
+    """One layer's attention while a video is generated in chunks of whole frames.
+
+    Every call takes the next frames' q, k and v [B, n * frame_tokens, heads, d] of B variants, as the
+    projection gives them. It norms and turns q and k at their place in the stream, appends k and v
+    to the variants' cache, and attends from the chunk's rows to
+      - the shared history (set_history): keys and values [Np, Hk, d] that all variants have in common,
+        stored and, where rows are few, read once for all of them;
+      - the variants' own cached frames and the chunk itself: frame-causal (a token sees its whole frame
+        and those before it), or the last `window` frames only. (The history is always seen.)
+    cap, slopes: as in lite_attn_span; distances count tokens of history and cache.
+
+    The cache holds `frames` frames; reset() empties it for the next video.
+    """
+
+    def __init__(self, rope: AxisRope, frames: int, frame_tokens: int, window: Optional[int] = None, cap: float = 0.0,
+                 slopes: Optional[torch.Tensor] = None, scale: Optional[float] = None):
+        if frames < 1 or frame_tokens < 1 or (window is not None and window < 1):
+            raise ValueError("frames, frame_tokens and window >= 1")
+        self.rope, self.frames, self.frame_tokens, self.window = rope, int(frames), int(frame_tokens), window
+        self.cap, self.slopes, self.scale = cap, slopes, scale
+        self._k = self._v = self._hk = self._hv = None
+        self._done = 0  # frames in the cache
+
+    def reset(self):
+        """The next call starts a new video (and may have another batch size); the history is dropped too."""
+        self._k = self._v = self._hk = self._hv = None
+        self._done = 0
+
+    @property
+    def cached_frames(self) -> int:
+        return self._done
+
+    def set_history(self, k: torch.Tensor, v: torch.Tensor):
+        """Shared history keys (normed and turned, bf16) and values [Np, Hk, d]; before the first chunk."""
+        if self._done:
+            raise ValueError("the history is set before the first chunk")
+        if k.dim() != 3 or k.shape != v.shape or k.dtype != torch.bfloat16 or v.dtype != torch.bfloat16:
+            raise ValueError("k and v must be bf16 tensors [Np, Hk, d] of one shape")
+        self._hk, self._hv = k, v
+
+    def __call__(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, start: Optional[int] = None,
+                 return_softmax_lse: bool = False):
+        """o [B, n * frame_tokens, H, d] of the chunk. start: grid index of the chunk's first token (default:
+        frames generated so far, after history of the same frame size)."""
+        B, N, _, d = q.shape
+        Hk = k.shape[2]
+        ft = self.frame_tokens
+        if N == 0 or N % ft:
+            raise ValueError(f"a chunk is a whole number of frames of {ft} tokens")
+        if v.shape != k.shape:
+            raise ValueError("k and v must have one shape")
+        n = N // ft
+        if self._done + n > self.frames:
+            raise ValueError(f"the cache holds {self.frames} frames: {self._done} are taken")
+        if self._k is None:
+            shape = (B, self.frames * ft, Hk, d)
+            self._k = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
+            self._v = torch.empty_like(self._k)
+        if (B, Hk, d) != (self._k.shape[0], self._k.shape[2], self._k.shape[3]):
+            raise ValueError("batch size, key heads and head dimension must stay as in the first chunk")
+        at, end = self._done * ft, (self._done + n) * ft
+        if start is None:
+            start = at + (0 if self._hk is None else self._hk.shape[0])
+        q, _ = self.rope(q, k, start=start, k_out=self._k[:, at:end])
+        self._v[:, at:end].copy_(v)
+        spans = None
+        if n > 1 or self.window is not None:
+            spans = frame_spans(n, ft, window=self.window, past=self._done, device=q.device)
+        kw = dict(scale=self.scale, cap=self.cap, slopes=self.slopes, return_lse=return_softmax_lse)
+        keys, values = self._k[:, :end], self._v[:, :end]
+        if self._hk is None:
+            o, lse = la.lite_attn_span(q, keys, values, spans, **kw)
+        else:
+            o, lse = la.lite_attn_prefix(q, self._hk, self._hv, keys, values, spans, **kw)
+        self._done += n
+        return (o, lse) if return_softmax_lse else o
 
 
 SplitAttn = Callable[[torch.Tensor, torch.Tensor, torch.Tensor, int], Tuple[torch.Tensor, torch.Tensor]]
