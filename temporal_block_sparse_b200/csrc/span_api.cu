@@ -230,7 +230,8 @@ double plan_us(const Plan& pl, int d, int64_t slots) {
     us = std::max(std::max(tp, to), (double(np) * tp + double(no) * to) / double(slots) + to * 0.5);
   if (pl.parts) {
     // the join: its launch, scratch and the parts' way through L2; passes of two kinds take a launch each
-    const double rows = 128.0 * 2.0 * (double(np) + double(no));
+    const auto rows_of = [](const PassPlan& ps, int64_t n) { return double(n) * (ps.F == 4 ? 32.0 : 256.0); };
+    const double rows = rows_of(pl.pre, np) + rows_of(pl.own, no);
     us += 8.0 + rows * (d * 4 + 8) * 2.0 / 4e6 + (np && no && pl.pre.F != pl.own.F ? 4.0 : 0.0);
   }
   return us;

@@ -107,6 +107,7 @@ struct SpanTile {
   int n_live, n_pre;
   int j_first;
   int q0, step;
+  int full_lo, full_hi;  // every row sees the own keys [full_lo, full_hi)
 };
 
 struct SpanInfo {
@@ -116,7 +117,6 @@ struct SpanInfo {
   int slot;              // index of its first part in scratch
   int v_first;
   uint32_t u0;           // union index of its first tile
-  int full_lo, full_hi;  // every row of both tiles sees the own keys [full_lo, full_hi)
   int n_bad;             // own key tiles whose non-finite values were taken out of shared memory (see
   int bad[kSpanBad];     // span_clean), the first kSpanBad of them by index
   SpanTile t[2];
@@ -133,35 +133,11 @@ __device__ __forceinline__ int span_union(const SpanInfo& it, int j, int q) {
          min(max(j - max(a.j_first, b.j_first), 0), both);
 }
 
-// Zeroes the infinities and NaN among this thread's 16-byte pieces of a V tile (pieces first, first + step,
-// ..); true if there were any.
-__device__ __forceinline__ bool span_clean(uint8_t* tile, int first, int step, int pieces) {
-  uint32_t most = 0u;  // largest magnitude of either half-word
-  for (int i = first; i < pieces; i += step) {
-    const uint4 x = *reinterpret_cast<const uint4*>(tile + i * 16);
-    most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
-  }
-  if ((most & 0xffffu) < 0x7f80u && (most >> 16) < 0x7f80u) return false;
-  for (int i = first; i < pieces; i += step) {
-    uint32_t* x = reinterpret_cast<uint32_t*>(tile + i * 16);
-#pragma unroll
-    for (int y = 0; y < 4; ++y) {
-      uint32_t w = x[y];
-      if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
-      if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
-      x[y] = w;
-    }
-  }
-  return true;
-}
-
 struct alignas(8) SpanCtl {
   uint64_t q_full, q_empty;
   uint64_t kv_full[2], kv_free[2];
   uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
   uint64_t item_full[2], item_empty[2];
-  uint64_t cleaned;      // both groups have cleaned their halves of a V tile
   uint64_t drain;
   uint32_t tmem_base;
   int abort;
@@ -209,7 +185,7 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
   const int ntok = prefix ? p.B * p.Nq : p.Nq;
   const int tp = (prefix || p.fused) ? p.Tp : 0;
   int jlo = 0x7fffffff, jhi = 0;  // own key tiles that either query tile has to see
-  int tlo[2] = {0, 0}, thi[2] = {0, 0}, full_lo[2] = {0, 0}, full_hi[2] = {p.Nk, p.Nk};  // and each of them
+  int tlo[2] = {0, 0}, thi[2] = {0, 0};  // and each of them
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     SpanTile& t = it.t[g];
@@ -221,6 +197,8 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
     }
     t.tok0 = (ps.alt ? pair : 2 * pair + g) * ps.TN;
     const int toks = max(0, min(ps.TN, ntok - t.tok0));
+    t.full_lo = 0;
+    t.full_hi = p.Nk;
     t.rows = toks * p.G;
     tlo[g] = thi[g] = 0;
     if (it.kind == 0 && toks > 0) {
@@ -250,19 +228,11 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
         jlo = min(jlo, tlo[g]);
         jhi = max(jhi, thi[g]);
       }
-      full_lo[g] = flo;
-      full_hi[g] = fhi;
+      t.full_lo = flo;
+      t.full_hi = fhi;
     }
   }
   if (jhi == 0) jlo = 0;
-  it.full_lo = 0;
-  it.full_hi = p.Nk;
-#pragma unroll
-  for (int g = 0; g < 2; ++g)
-    if (thi[g] > tlo[g]) {
-      it.full_lo = max(it.full_lo, full_lo[g]);
-      it.full_hi = min(it.full_hi, full_hi[g]);
-    }
   // virtual tiles: prefix [0, tp), then own jlo .. jhi; this split's are [v0, v1)
   const long long total = tp + (jhi - jlo);
   const int v0 = int(total * split / ps.splits), v1 = int(total * (split + 1) / ps.splits);
@@ -280,29 +250,43 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
   }
 }
 
-// This thread's part in cleaning own key tile j (entry q of its group's list): both groups have a half of it each
-// when both compute it, and then true, for neither may have its product before both are done.
+// This thread's part of a group's cleaning of own key tile j (entry q of its list): the tile goes into the item's
+// list, then its infinities and NaN become 0. The other group may use the tile at the same time: if it needs
+// it clean it cleans it too (a value is 0 then before either product that must not see it), and if its
+// rows see these values, the list, written first, brings them back.
 template <typename C, int BN>
-__device__ __noinline__ bool span_clean_tile(SpanCtl* ctl, uint8_t* smem, const Waiter& wt, int slot, int grp, int tid,
-                                             int j, int q) {
+__device__ __forceinline__ void span_clean_tile(SpanCtl* ctl, uint8_t* smem, const Waiter& wt, int slot, int tid, int j, int q) {
   SpanInfo& it = ctl->info[slot];
   const uint32_t u = it.u0 + span_union(it, j, q);
-  const SpanTile& other = it.t[grp ^ 1];
-  const bool both = !it.alt && j >= other.j_first && j < other.j_first + other.n_live - other.n_pre;
   wt.wait(ptx::smem_addr(&ctl->kv_full[(u + 1) & 1]), ((u + 1) >> 1) & 1);  // V_u comes with bundle u + 1
-  if (!span_clean(smem + C::OFF_V + (u & 1) * C::KV_BYTES, both ? grp * 128 + tid : tid, both ? 256 : 128,
-                  C::KV_BYTES / 16))
-    return both;
-  ptx::fence_proxy_async_smem();
-  for (int x = 0; x < kSpanBad; ++x) {
-    const int old = atomicCAS(&it.bad[x], -1, j);
-    if (old == -1 || old == j) {
-      atomicMax(&it.n_bad, x + 1);
-      return both;
+  volatile uint4* const tile = reinterpret_cast<volatile uint4*>(smem + C::OFF_V + (u & 1) * C::KV_BYTES);
+  constexpr int PIECES = C::KV_BYTES / 16 / 128;  // 16-byte pieces of a thread
+  uint32_t most = 0u;  // largest magnitude of either half-word
+#pragma unroll 4
+  for (int i = 0; i < PIECES; ++i) {
+    const uint4 x = *reinterpret_cast<const uint4*>(const_cast<const uint4*>(tile + i * 128 + tid));
+    most = __vmaxu2(most, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                   __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+  }
+  if ((most & 0xffffu) >= 0x7f80u || (most >> 16) >= 0x7f80u) {
+    int x = 0;
+    for (; x < kSpanBad; ++x) {
+      const int old = atomicCAS(&it.bad[x], -1, j);
+      if (old == -1 || old == j) break;
+    }
+    atomicMax(&it.n_bad, x + 1);  // kSpanBad + 1: the list is full
+    __threadfence_block();
+    for (int i = 0; i < PIECES; ++i) {
+      volatile uint32_t* const w = reinterpret_cast<volatile uint32_t*>(tile + i * 128 + tid);
+      for (int y = 0; y < 4; ++y) {
+        uint32_t z = w[y];
+        if ((z & 0x7f80u) == 0x7f80u) z &= 0xffff0000u;
+        if ((z & 0x7f800000u) == 0x7f800000u) z &= 0xffffu;
+        w[y] = z;
+      }
     }
   }
-  atomicMax(&it.n_bad, kSpanBad + 1);
-  return both;
+  ptx::fence_proxy_async_smem();  // also for what the other group wrote and this thread read
 }
 
 // Shared memory: lite_attn_kernel's layout, with a staging area of 32 rows x 128 bytes a softmax warp.
@@ -402,9 +386,8 @@ __device__ __forceinline__ void span_rescale(uint32_t o_tmem, float alpha) {
 // A key tile for which the short way does not do (a span ends in it, scores near the cap, rows on both sides of it,
 // given positions): every score of the warp's rows in full, back into TMEM, then the exponentials. Keys
 // [lo, hi) of this thread's NC columns are seen. Takes and returns (reference, row sum).
-// Out of line, for the registers of the tiles that need none of it.
 template <int D, int NC, int MOD, int F>
-__device__ __noinline__ float2 span_tile_in_full(const SpanParams& p, uint32_t s_tmem, uint32_t o_tmem, int quarter,
+__device__ __forceinline__ float2 span_tile_in_full(const SpanParams& p, uint32_t s_tmem, uint32_t o_tmem, int quarter,
                                                  int lo, int hi, float base, float slope, float qp, const float* kpos,
                                                  float2 ml, bool rescale) {
   constexpr bool CAP = (MOD & kSpanCap) != 0, BIAS = (MOD & kSpanBias) != 0;
@@ -423,19 +406,39 @@ __device__ __noinline__ float2 span_tile_in_full(const SpanParams& p, uint32_t s
     const uint32_t bits = upto & ~below;
     const float at = base + float(PC * c);
     const float* kc = kpos + PC * c;
+    if constexpr (CAP) {
+      float big = 0.f;
+#pragma unroll
+      for (int x = 0; x < PC; x += 2) big = abs_max3(big, v[x], v[x + 1]);
+      const bool all_near = !__any_sync(0xffffffffu, big > p.cap_mid);
+#pragma unroll
+      for (int x = 0; x < PC; x += 2) {
+        const float2 s2 = make_float2(v[x], v[x + 1]);
+        const float2 y = __fmul2_rn(s2, s2);
+        float2 t = __ffma2_rn(make_float2(p.cap_b[4], p.cap_b[4]), y, make_float2(p.cap_b[3], p.cap_b[3]));
+        t = __ffma2_rn(t, y, make_float2(p.cap_b[2], p.cap_b[2]));
+        t = __ffma2_rn(t, y, make_float2(p.cap_b[1], p.cap_b[1]));
+        t = __ffma2_rn(t, y, make_float2(p.cap_b[0], p.cap_b[0]));
+        t = __fmul2_rn(s2, t);
+        if (!all_near) {
+          // cap tanh(z) = cap - 2 cap / (1 + e^{2z}), in log2 units; both ends saturate exactly. Near zero it
+          // cancels (a large cap against small scores), there the polynomial stays.
+          const float fx = fmaf(-2.f * p.cap_c, fast_rcp(1.f + ptx::ex2(s2.x * p.cap_a)), p.cap_c);
+          const float fy = fmaf(-2.f * p.cap_c, fast_rcp(1.f + ptx::ex2(s2.y * p.cap_a)), p.cap_c);
+          t.x = fabsf(s2.x) <= p.cap_mid ? t.x : fx;
+          t.y = fabsf(s2.y) <= p.cap_mid ? t.y : fy;
+        }
+        v[x] = t.x;
+        v[x + 1] = t.y;
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < PC; ++x) v[x] *= p.scale_log2;
+    }
 #pragma unroll
     for (int x = 0; x < PC; ++x) {
-      float t = v[x] * p.scale_log2;
-      if (CAP) {
-        // cap tanh(z) = cap - 2 cap / (1 + e^{2z}), in log2 units; both ends saturate exactly. Near zero it cancels
-        // (a large cap against small scores), and the polynomial takes over.
-        const float y = v[x] * v[x];
-        const float far = fmaf(-2.f * p.cap_c, fast_rcp(1.f + ptx::ex2(v[x] * p.cap_a)), p.cap_c);
-        t = v[x] * fmaf(fmaf(fmaf(fmaf(p.cap_b[4], y, p.cap_b[3]), y, p.cap_b[2]), y, p.cap_b[1]), y, p.cap_b[0]);
-        t = fabsf(v[x]) <= p.cap_mid ? t : far;
-      }
-      if (BIAS) t = fmaf(-slope, fabsf(kpos ? kc[x] - qp : at + float(x)), t);
-      v[x] = (bits & (1u << x)) ? t : -INFINITY;
+      if (BIAS) v[x] = fmaf(-slope, fabsf(kpos ? kc[x] - qp : at + float(x)), v[x]);
+      v[x] = (bits & (1u << x)) ? v[x] : -INFINITY;
     }
     span_max<PC>(v, m);
     if constexpr (PC == 32)
@@ -471,7 +474,7 @@ __device__ __noinline__ float2 span_tile_in_full(const SpanParams& p, uint32_t s
 // Adds the non-finite values of the keys [ks, ke) that this thread's row sees (columns col0 .. col0 + NC of each
 // tile) to its row of O: those of the tiles that were cleaned for the item.
 template <int D, int BN, int NC>
-__device__ __noinline__ void span_repair(const SpanParams& p, const SpanInfo& it, uint32_t o_tmem, bool valid, int ks,
+__device__ __forceinline__ void span_repair(const SpanParams& p, const SpanInfo& it, uint32_t o_tmem, bool valid, int ks,
                                          int ke, int b, int col0) {
   // more tiles than the list holds: all tiles of the row's span
   const bool listed = it.n_bad <= kSpanBad;
@@ -539,7 +542,6 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       ptx::mbar_init(BAR(item_full[b]), 1);
       ptx::mbar_init(BAR(item_empty[b]), 8);
     }
-    ptx::mbar_init(BAR(cleaned), 256);
     ptx::mbar_init(BAR(drain), 1);
     ctl->abort = 0;
     ptx::fence_mbar_init();
@@ -793,7 +795,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
       }
       h = it->hk * p.G + r_head;
     };
-    uint32_t tg = 0, items = 0, pv_phase = 0, cleaned = 0;
+    uint32_t tg = 0, items = 0, pv_phase = 0;
     while (true) {
       const int slot = items & 1;
       bool ok = wt.wait(BAR(item_full[slot]), (items >> 1) & 1);
@@ -842,7 +844,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           ptx::named_bar_sync(gbar, 128);
         }
         if (BIAS && idx + 1 < n_live) kp_next = key_pos(idx + 1);
-        const bool masked = pre ? p.Np - j0 < BN : (it->full_lo > j0 || it->full_hi < j0 + BN);
+        const bool masked = pre ? p.Np - j0 < BN : (mt->full_lo > j0 || mt->full_hi < j0 + BN);
         wt.wait(BAR(s_full[grp]), tg & 1);
         ++tg;
         __syncwarp();
@@ -966,15 +968,11 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
             l = ml.y;
           }
         }
-        if (masked && !pre && (it->full_lo > j0 || it->full_hi < min(j0 + BN, p.Nk))) {
+        if (masked && !pre && (mt->full_lo > j0 || mt->full_hi < min(j0 + BN, p.Nk))) {
           // Some rows do not see all keys of this tile. Their P is 0 there, but 0 times an infinity or NaN is
           // NaN: such values (whatever lies behind a sequence's end, say) are taken out of V before the
           // product, and rows that do see them get them back in the epilogue.
-          if (span_clean_tile<C, BN>(ctl, smem, wt, slot, grp, quarter * 32 + lane, j0 / BN, entry)) {
-            ptx::mbar_arrive(BAR(cleaned));
-            wt.wait(BAR(cleaned), cleaned & 1);
-            ++cleaned;
-          }
+          span_clean_tile<C, BN>(ctl, smem, wt, slot, quarter * 32 + lane, j0 / BN, entry);
           __syncwarp();
         }
         ptx::tc_fence_before();
