@@ -211,18 +211,26 @@ PassPlan make_pass(int64_t units, int64_t tokens, int G, int64_t tiles) {
 }
 
 // Microseconds that one CTA takes for an item of t key tiles: its start and end, and each tile, as
-// measured on a B200 with all CTAs busy (a d = 64 tile has half the keys and shares its SM).
-double item_us(const PassPlan& ps, int d, int64_t t) {
-  const double tile = ps.F == 4 ? (d == 64 ? 1.0 : 1.35) : ps.alt ? (d == 64 ? 0.9 : 1.4) : (d == 64 ? 1.75 : 2.4);
-  return 4.0 + tile * double(t);
+// measured on a B200 with few CTAs and with all of them busy (a d = 64 tile has half the keys and shares
+// its SM).
+double item_us(const PassPlan& ps, int d, double t, bool busy) {
+  double tile;
+  if (ps.F == 4)
+    tile = d == 64 ? (busy ? 1.0 : 0.75) : (busy ? 1.35 : 1.05);
+  else if (ps.alt)
+    tile = d == 64 ? (busy ? 0.9 : 0.7) : (busy ? 1.4 : 1.1);
+  else
+    tile = d == 64 ? (busy ? 1.75 : 1.25) : (busy ? 2.4 : 2.1);
+  return 4.0 + tile * t;
 }
 
 // Time of both passes' items on `slots` CTAs: whole waves where all items are alike, else the
-// bound of list scheduling.
+// bound of list scheduling. (The spans are on the device: every query tile counts with all keys.)
 double plan_us(const Plan& pl, int d, int64_t slots) {
   const int64_t np = pl.pre.items(), no = pl.own.items();
-  const double tp = np ? item_us(pl.pre, d, ceil_div(pl.pre.tiles, pl.pre.splits)) : 0.0;
-  const double to = no ? item_us(pl.own, d, ceil_div(pl.own.tiles, pl.own.splits)) : 0.0;
+  const bool busy = 2 * (np + no) > slots;
+  const double tp = np ? item_us(pl.pre, d, double(ceil_div(pl.pre.tiles, pl.pre.splits)), busy) : 0.0;
+  const double to = no ? item_us(pl.own, d, double(ceil_div(pl.own.tiles, pl.own.splits)), busy) : 0.0;
   double us;
   if (np == 0 || no == 0)
     us = double(ceil_div(np + no, slots)) * std::max(tp, to);
