@@ -13,7 +13,8 @@ LiteAttention that is given one takes the projection's q and k as they are. Chun
 generates a video frame by frame: each call's frames attend to a shared history, to the frames
 before them (kept in its key and value cache) and to themselves.
 
-Host bookkeeping only: every tensor operation runs in the CUDA library through lite_attn. The
+Host bookkeeping only: every tensor operation runs in the CUDA library through lite_attn (but for the copy of
+v into ChunkedAttention's cache). The
 state is a pair of mask buffers per (split, shape); each call reads one and writes the other (the
 library copies mask_in into mask_out and ORs new flags), then the pair swaps.
 """

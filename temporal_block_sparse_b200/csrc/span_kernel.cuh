@@ -14,16 +14,28 @@
 // tokens of different batch entries (the prefix pass takes the batch as one row of B * Nq tokens),
 // so the prefix is read once for the batch.
 //
-// Work items. An item is a pair of query tiles (one per softmax warpgroup) and a part of the key
-// tiles they see: [prefix tiles][own tiles lo .. hi), of which split s of S takes its share. With
-// S = 1 and one pass the item writes o and lse; otherwise it writes its unnormalised O, row maximum
-// and row sum (32-bit) to scratch, and lite_span_combine_kernel joins the parts in index order.
+// Up to 32 rows (F = 4) leave three quarters of the MMA's rows empty: they are loaded four times, into
+// the lanes of all four warps of a softmax group, and each warp takes a fourth of the tile's key
+// columns. Where there is one query tile only, both softmax groups take it, on alternate key
+// tiles (`alt`), and this tile's QK^T is issued before the product of the other group's tile. With F = 4
+// the eight partial results of a row are joined in the CTA. One token of 8 sequences of up to 32760
+// keys (40 heads over 8, d = 128, 839 MB): 249 us with one group and one warp at work, 169 us so.
+//
+// Work items. An item is a pair of query tiles (one per softmax warpgroup), or one tile (alt), and a
+// part of the key tiles they see: [prefix tiles][own tiles lo .. hi), of which split s of S takes its
+// share. With S = 1 and one pass the item writes o and lse; otherwise it writes its unnormalised O, its
+// exponents' reference and its row sum (32-bit) to scratch, and lite_span_combine_kernel joins the
+// parts in index order.
 //
 // Warp roles (320 threads), barriers and the S -> P -> PV chain are those of lite_attn_kernel
 // (attn_kernel.cuh): warp 0 finds the key range of the item's rows and feeds K and V by TMA, warp 1
 // issues the MMAs, warps 2-5 and 6-9 run the softmax of one query tile each, P staying in TMEM.
-// A key tile that every row of the query tile sees entirely takes no mask instruction; only tiles
-// that a span ends in (and the last one) pay for the comparison.
+// A key tile that every row of the query tile sees entirely takes no mask instruction.
+//
+// What bounds it. Long rows: the S -> P -> PV -> QK chain of each query tile, as in lite_attn_kernel
+// (frame-causal 480p layer, 40 heads, d = 128: 11.5 ms, 1000 TFLOP/s; tensor pipe 47% busy, exponential
+// unit 47%, issue slots 33%). d = 64: the exponential unit and issue slots. Few rows: HBM (839 MB in
+// 150 us, 5.6 TB/s). Small calls: launches.
 //
 // Every wait is bounded as in lite_attn_kernel; on expiry the status word is set and the CTA drains.
 #pragma once
@@ -93,7 +105,7 @@ struct SpanParams {
   float cap_b[5];           // its coefficients in s^2
 };
 
-// floats of one part: O rows, then row maxima and row sums of a 128-row tile
+// floats of one part: O rows, then the rows' references and sums, of a 128-row tile
 template <int D>
 struct SpanPart {
   static constexpr size_t FLOATS = 128 * D + 256;
