@@ -452,8 +452,8 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream);
  *  Nq <= 2^24. Nk = 0 is refused here (lite_attn_prefix allows it).
  *
  * Calls with few query tiles split the keys over the SMs and join the parts with a second kernel; the
- * parts (and a work counter) come from the library's stream-ordered pool. Results do not depend on
- * timing: two equal calls give equal bits.
+ * parts (and a work counter), a gigabyte at most, come from the library's stream-ordered pool. Results do
+ * not depend on timing: two equal calls give equal bits.
  */
 typedef struct lite_span_args {
   const void* q;

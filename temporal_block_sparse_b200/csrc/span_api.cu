@@ -240,6 +240,7 @@ double plan_us(const Plan& pl, int d, int64_t slots) {
     // the join: its launch, scratch and the parts' way through L2; passes of two kinds take a launch each
     const auto rows_of = [](const PassPlan& ps, int64_t n) { return double(n) * (ps.F == 4 ? 32.0 : 256.0); };
     const double rows = rows_of(pl.pre, np) + rows_of(pl.own, no);
+    if (rows * (d * 4 + 8) > double(1 << 30)) return 1e30;  // no more than a gigabyte of scratch
     us += 8.0 + rows * (d * 4 + 8) * 2.0 / 4e6 + (np && no && pl.pre.F != pl.own.F ? 4.0 : 0.0);
   }
   return us;

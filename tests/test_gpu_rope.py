@@ -85,3 +85,76 @@ def test_in_place_and_into_a_cache_slice():
     la.lite_qk_rope(q2, k, plan, grid=(3, 1, 7), q_weight=w, k_weight=w, q_out=q2, k_out=cache[:, 9 : 9 + N])
     assert torch.equal(q2, yq) and torch.equal(cache[:, 9 : 9 + N], yk)
     assert (cache[:, :9] == 7).all() and (cache[:, 9 + N :] == 7).all()
+
+
+@pytest.mark.parametrize("B,N,H,Hk,d,dtype", [
+    (300, 2, 20, 20, 128, torch.bfloat16),   # a block passes several batch entries from one step to the next
+    (700, 1, 40, 1, 64, torch.float16),      # many tokens a block for the one key head, one for the queries
+    (1, 3, 128, 128, 128, torch.float32),    # the widest row
+    (2, 3, 256, 1, 64, torch.bfloat16),
+    (1, 5000, 1, 1, 64, torch.float32)])
+@pytest.mark.parametrize("norm", ["head", "row"])
+def test_many_entries_and_wide_rows(B, N, H, Hk, d, dtype, norm):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(B + H)
+    q = torch.randn(B, N, H, d, generator=g, device="cuda").to(dtype)
+    k = torch.randn(B, N, Hk, d, generator=g, device="cuda").to(dtype)
+    plan = la.RopePlan(wl.axis_split(d))
+    wq, wk = (1 + 0.2 * torch.randn(n, generator=g, device="cuda") for n in ((d, d) if norm == "head" else (H * d, Hk * d)))
+    # cells past 2^40 of a huge grid, so that the index takes 64 bits
+    grid, start = (1 << 40, 50, 100), (1 << 30) * 5000 + 123
+    yq, yk = la.lite_qk_rope(q, k, plan, grid=grid, start=start, q_weight=wq, k_weight=wk)
+    at = np.broadcast_to(ref.grid_positions(grid, start, N), (B, 3, N))
+    # positions of 2^30 x frequency: the oracle's own product is off by 2^-53 of 2^30 turns, 10^-7
+    for x, y, w in ((q, yq, wq), (k, yk, wk)):
+        check(y, ref.rope(x.double().cpu().numpy(), at, plan.freq, plan.axis, "interleaved", w.double().cpu().numpy()),
+              "interleaved")
+
+
+def test_queries_alone_with_norm_and_negative_positions():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    q = torch.randn(2, 9, 3, 64, generator=g, device="cuda").to(torch.bfloat16)
+    plan, w = la.RopePlan((64,), pairing="half"), torch.rand(3 * 64, generator=g, device="cuda")
+    pos = torch.arange(-4, 5, dtype=torch.int32, device="cuda")[None] * 1000
+    y, _ = la.lite_qk_rope(q, None, plan, pos=pos, q_weight=w)
+    at = np.broadcast_to(pos.double().cpu().numpy(), (2, 1, 9))
+    check(y, ref.rope(q.double().cpu().numpy(), at, plan.freq, plan.axis, "half", w.double().cpu().numpy()), "half")
+
+
+def test_captured_and_on_two_streams():
+    g = torch.Generator(device="cuda")
+    g.manual_seed(4)
+    q, k = (torch.randn(1, 2000, h, 128, generator=g, device="cuda").to(torch.bfloat16) for h in (12, 3))
+    plan = la.RopePlan(wl.axis_split(128))
+    want = la.lite_qk_rope(q, k, plan, grid=(2, 25, 40))
+    out = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        la.lite_qk_rope(q, k, plan, grid=(2, 25, 40), q_out=out[0], k_out=out[1])
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [la.lite_qk_rope(q, k, plan, grid=(2, 25, 40), stream=s) for s in streams]
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in got + [out]:
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
+
+
+def test_python_refusals():
+    q = torch.zeros(1, 4, 2, 64, dtype=torch.bfloat16, device="cuda")
+    plan = la.RopePlan((24, 20, 20))
+    w = torch.ones(64, device="cuda")
+    for bad in (dict(grid=(1, 2, 3), start=3), dict(grid=(1, 2, 3), start=-1), dict(grid=(2, 2)), dict(),
+                dict(grid=(2, 2, 2), pos=torch.zeros(3, 4, device="cuda")), dict(pos=torch.zeros(2, 4, device="cuda")),
+                dict(pos=torch.zeros(3, 4, device="cuda").double()), dict(grid=(2, 2, 2), q_weight=w),
+                dict(grid=(2, 2, 2), q_weight=w, k_weight=torch.ones(128, device="cuda")),
+                dict(grid=(2, 2, 2), q_weight=w[1:].repeat(3)[:64], k_weight=w.half()),
+                dict(grid=(2, 2, 2), q_weight=w, k_weight=w, eps=-1.0), dict(grid=(2, 2, 2), q_out=q.float()),
+                dict(grid=(2, 2, 2), q_out=q[:, :3]), dict(grid=(0, 2, 2))):
+        with pytest.raises(ValueError):
+            la.lite_qk_rope(q, q, plan, **bad)
+    with pytest.raises(ValueError):
+        la.lite_qk_rope(q, q.half(), plan, grid=(2, 2, 2))
+    with pytest.raises(ValueError):
+        la.lite_qk_rope(q, q, la.RopePlan((44, 42, 42)), grid=(2, 2, 2))

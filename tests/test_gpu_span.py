@@ -342,3 +342,43 @@ def test_a_stalled_kernel_gives_up_and_says_so():
     for x, w in zip((q, q1), want):
         got = la.lite_attn_span(x, k, v)
         assert torch.equal(got[0], w[0]) and torch.equal(got[1], w[1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_many_items_of_few_rows(d):
+    # more items than CTAs, handed out one by one; row counts on both sides of 32
+    lengths = [(37 * b) % 300 for b in range(48)]
+    span_case(48, 1, 300, 8, 8, d, sp.padded_spans(lengths, 1), seed=1)
+    span_case(12, 32, 140, 16, 16, d, sp.padded_spans(lengths[:12], 32, causal=True), seed=2)
+    span_case(12, 33, 140, 16, 16, d, sp.padded_spans(lengths[:12], 33, causal=True), seed=3)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_prefix_pass_and_own_pass_of_different_kinds(d):
+    # 64 stacked rows against the prefix, 8 rows of each sequence against its own keys
+    B, Nq, Nk, Np, H = 8, 8, 60, 6000, 20
+    q, k, v, kp, vp = make(d, (B, Nq, H, d), (B, Nk, H, d), (B, Nk, H, d), (Np, H, d), (Np, H, d))
+    spans = sp.padded_spans([60, 1, 0, 33, 8, 59, 60, 17], Nq, causal=True)
+    o, lse = la.lite_attn_prefix(q, kp, vp, k, v, spans, return_lse=False)
+    assert lse is None
+    check((o, None), ref.span_attention(f64(q), f64(k), f64(v), f64(spans), f64(kp), f64(vp)))
+
+
+def test_outputs_given_and_rows_outside_them_untouched():
+    q, k, v = make(5, (2, 70, 3, 64), (2, 90, 3, 64), (2, 90, 3, 64))
+    want = la.lite_attn_span(q, k, v)
+    big = torch.full((4, 70, 3, 64), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((4, 3, 70), 5.0, device="cuda")
+    got = la.lite_attn_span(q, k, v, o=big[1:3], lse=lse[1:3])
+    assert got[0].data_ptr() == big[1:3].data_ptr()
+    assert torch.equal(big[1:3], want[0]) and torch.equal(lse[1:3], want[1])
+    assert (big[0] == 5).all() and (big[3] == 5).all() and (lse[0] == 5).all() and (lse[3] == 5).all()
+    for bad in (dict(o=big), dict(o=big[1:3].float()), dict(lse=lse), dict(spans=torch.zeros(70, 2, device="cuda")),
+                dict(spans=torch.zeros(3, 70, 2, dtype=torch.int32, device="cuda")), dict(cap=-1.0),
+                dict(slopes=torch.zeros(2, device="cuda")), dict(q_pos=torch.zeros(70, device="cuda"))):
+        with pytest.raises(ValueError):
+            la.lite_attn_span(q, k, v, **bad)
+    with pytest.raises(ValueError):
+        la.lite_attn_span(q, k[..., ::2], v[..., ::2])
+    with pytest.raises(ValueError):
+        la.lite_attn_span(q, k[:, :, :2], v[:, :, :2])
