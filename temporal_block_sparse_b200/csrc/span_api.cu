@@ -412,17 +412,22 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   const float scale = (a.scale > 0.f && !std::isnan(a.scale)) ? a.scale : 1.0f / std::sqrt(float(a.d));
   p.scale_log2 = scale * 1.4426950408889634f;
   if (a.cap > 0.f) {
-    p.cap_a = 2.f * p.scale_log2 / a.cap;
+    p.cap_a = std::min(2.f * p.scale_log2 / a.cap, 3e38f);
     p.cap_c = a.cap * 1.4426950408889634f;
     // tanh(z) / z on |z| <= 0.6 as a polynomial in z^2: the least largest relative error (7.3e-8) of
     // degree 4, fitted numerically; z = s scale / cap
     const double c[5] = {0.999999927, -0.3333231, 0.133101736, -0.0521014795, 0.0154754266};
     const double zs = double(scale) / a.cap;
-    // (and not so large that a row's reference, the largest |score|, is far from its maximum: 24 in log2 units)
-    p.cap_mid = float(0.6 / zs);
-    p.cap_near = float(std::min(0.6 / zs, 24.0 / (double(scale) * 1.4426950408889634)));
-    double f = double(scale) * 1.4426950408889634;
-    for (int x = 0; x < 5; ++x, f *= zs * zs) p.cap_b[x] = float(c[x] * f);
+    if (zs > 1e4) {
+      // a cap next to nothing: its coefficients would leave the 32-bit range, and the other form is as exact
+      p.cap_mid = p.cap_near = -1.f;
+    } else {
+      p.cap_mid = float(0.6 / zs);
+      // (and not so large that a row's reference, the largest |score|, is far from its maximum: 24 in log2 units)
+      p.cap_near = float(std::min(0.6 / zs, 24.0 / (double(scale) * 1.4426950408889634)));
+      double f = double(scale) * 1.4426950408889634;
+      for (int x = 0; x < 5; ++x, f *= zs * zs) p.cap_b[x] = float(c[x] * f);
+    }
   }
   // Scratch: work counters where there are more items than CTAs (their lengths depend on the spans), and
   // the parts.

@@ -382,3 +382,13 @@ def test_outputs_given_and_rows_outside_them_untouched():
         la.lite_attn_span(q, k[..., ::2], v[..., ::2])
     with pytest.raises(ValueError):
         la.lite_attn_span(q, k[:, :, :2], v[:, :, :2])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,scale", [(1e-30, None), (1e-9, None), (1e-4, 100.0), (3e38, None), (40.0, 1e-6)])
+def test_caps_and_scales_at_the_ends_of_the_range(d, cap, scale):
+    # a cap next to nothing makes all scores equal, an enormous one changes none
+    q, k, v = make(13, (1, 130, 2, d), (1, 260, 2, d), (1, 260, 2, d))
+    for spans in (None, sp.padded_spans([200], 130)):
+        want = ref.span_attention(f64(q), f64(k), f64(v), f64(spans), cap=cap if cap < 1e30 else 0.0, scale=scale)
+        check(la.lite_attn_span(q, k, v, spans, cap=cap, scale=scale), want)
