@@ -18,10 +18,10 @@
 // need no barrier), and their angles are computed beside the present work: one barrier per step is
 // left (none, but for new angles, without a row norm), and the loads never stop.
 //
-// Measured (B200, 6.55 TB/s copy): 720p layer, 75600 tokens x 2 x 40 heads, d = 128, bf16, row norm: 565-605 us
-// for 3.10 GB (0.78-0.84 of the copy); 480p, d = 64, fp32 in, head norm: 155-170 us for 1.01 GB (0.91-0.99).
-// Fewer blocks with more registers (128) beat more blocks (64 registers: 15% slower), two stages three
-// or four (1-20%). The row norm's barrier keeps the first from the second's rate.
+// Measured (B200, 6.55 TB/s copy): 720p layer, 75600 tokens x 2 x 40 heads, d = 128, bf16, row norm: 565-613 us
+// for 3.10 GB (0.77-0.84 of the copy); 480p, d = 64, fp32 in, head norm: 155-170 us for 1.01 GB (0.91-0.99).
+// Fewer blocks with more registers (128) beat more blocks (64 registers: 15% slower), fewer stages more
+// (see RopeCfg). The row norm's barrier keeps the first from the second's rate.
 //
 // Angles are formed in 64 bits and reduced to half a turn either way before they become 32-bit
 // numbers: positions of a long stream reach 10^5 and more, where a 32-bit angle is off by 10^-2. For whole
@@ -137,12 +137,13 @@ __device__ __forceinline__ void rope_positions(const RopeParams& p, int t, long 
   }
 }
 
-constexpr int kRopeStages = 2;  // steps whose data are in shared memory or on their way
-
 template <typename T, int U>
 struct RopeCfg {
   static constexpr int E = 16 / sizeof(T);   // elements of a piece
   static constexpr int RC = 16 / E;          // pieces of a unit
+  // Steps whose data are in shared memory or on their way. With 16-bit inputs three (a frame of 2 x 1560 tokens: 26.7
+  // us, 28.7 with two; the 720p layer within 1%), with fp32 two (480p: 155-170 us, 178 with three).
+  static constexpr int STAGES = sizeof(T) == 2 ? 3 : 2;
   static constexpr int STEP = U * RC * 16;   // bytes of a thread's step
 };
 
@@ -156,8 +157,8 @@ struct RopeShape {
   int threads;
   __host__ __device__ int slots() const { return ahead * tpb; }
   __host__ __device__ int sums(int heads) const { return (tpb * heads > 32 ? tpb * heads : 32); }
-  __host__ __device__ size_t bytes(int step, int D, int heads) const {
-    return size_t(kRopeStages) * step * threads + (D / 2) * 12 +
+  __host__ __device__ size_t bytes(int data, int D, int heads) const {  // data: bytes of a thread's pieces
+    return size_t(data) * threads + (D / 2) * 12 +
            2 * (size_t(slots()) * (kRopeMaxAxes * 8 + D * 4) + size_t(sums(heads)) * 4);
   }
 };
@@ -178,7 +179,7 @@ __global__ void __maxnreg__(128) lite_rope_kernel(const __grid_constant__ RopePa
   const int tid = threadIdx.x, threads = sh.threads, lane = tid & 31, warp = tid >> 5;
   if (tid >= threads) return;  // (the other tensor's blocks are larger); barriers count `threads`
   uint8_t* const pieces = rope_smem + tid * 16;
-  double* const turns = reinterpret_cast<double*>(rope_smem + kRopeStages * R::STEP * threads);
+  double* const turns = reinterpret_cast<double*>(rope_smem + R::STAGES * R::STEP * threads);
   int* const axis = reinterpret_cast<int*>(turns + D / 2);
   long long* const places = reinterpret_cast<long long*>(axis + D / 2);  // [2][slots][axes]
   const int slots = sh.slots();
@@ -269,7 +270,7 @@ __global__ void __maxnreg__(128) lite_rope_kernel(const __grid_constant__ RopePa
     dst_at = place(int(first), x.y, x.ys, head[0], 2);
   }
 #pragma unroll
-  for (int y = 0; y < kRopeStages - 1; ++y) load(first + static_cast<long long>(y) * stride, y);
+  for (int y = 0; y < R::STAGES - 1; ++y) load(first + static_cast<long long>(y) * stride, y);
   // weights of the thread's units: they stay in registers
   float4 w[NORM ? U : 1][4];
   if constexpr (NORM != 0) {
@@ -296,8 +297,8 @@ __global__ void __maxnreg__(128) lite_rope_kernel(const __grid_constant__ RopePa
   int stage = 0, in_table = 0, table = 0;  // place of the step in its angle table, and which of the two
   for (int step = 0; first < p.tokens; first += stride, ++step) {
     // the stage loaded into was read by this thread in the step before
-    load(first + static_cast<long long>(kRopeStages - 1) * stride, stage == 0 ? kRopeStages - 1 : stage - 1);
-    rope_copies_left<kRopeStages - 1>();
+    load(first + static_cast<long long>(R::STAGES - 1) * stride, stage == 0 ? R::STAGES - 1 : stage - 1);
+    rope_copies_left<R::STAGES - 1>();
     float* hsum = sums + (step & 1) * sh.sums(heads);
     uint4 raw[U][R::RC];
     float ss[U];
@@ -402,7 +403,7 @@ __global__ void __maxnreg__(128) lite_rope_kernel(const __grid_constant__ RopePa
       for (int c = 0; c < R::RC; ++c) rope_put<P2>(dst + c * (D / R::RC) * 2, y + c * P2);
     }
     if (ONE && first + stride < p.tokens) advance(dst_at, int(first) + stride, out_step, x.y, x.ys, 2);
-    stage = stage + 1 == kRopeStages ? 0 : stage + 1;
+    stage = stage + 1 == R::STAGES ? 0 : stage + 1;
     if (++in_table == sh.ahead) {
       in_table = 0;
       table ^= 1;

@@ -64,8 +64,9 @@ int launch_rope(lite::RopeParams p, const DeviceContext& dc, cudaStream_t stream
   const lite::RopeShape sq = rope_shape(p.t[0].heads, D, U), sk = rope_shape(std::max(p.t[1].heads, 1), D, U);
   const bool keys = p.t[1].heads > 0;
   const int threads = keys ? std::max(sq.threads, sk.threads) : sq.threads;
-  size_t smem = sq.bytes(lite::RopeCfg<T, U>::STEP, D, p.t[0].heads);
-  if (keys) smem = std::max(smem, sk.bytes(lite::RopeCfg<T, U>::STEP, D, p.t[1].heads));
+  using R = lite::RopeCfg<T, U>;
+  size_t smem = sq.bytes(R::STAGES * R::STEP, D, p.t[0].heads);
+  if (keys) smem = std::max(smem, sk.bytes(R::STAGES * R::STEP, D, p.t[1].heads));
   if (smem > 48 * 1024 &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
     return LITE_ERR_CUDA;
