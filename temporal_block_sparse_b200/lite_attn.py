@@ -551,6 +551,7 @@ class RopePlan:
         self._halves = int(pairing == "half")
 
 
+_POS_TYPES = {torch.float32: LITE_FP32, torch.int32: LITE_INT32}
 _ROPE_TYPES = {torch.bfloat16: LITE_BF16, torch.float16: LITE_FP16, torch.float32: LITE_FP32}
 
 
@@ -605,11 +606,12 @@ def lite_qk_rope(q: torch.Tensor, k: Optional[torch.Tensor], plan: RopePlan, gri
     else:
         if start:
             raise ValueError("start belongs to grid")
-        if (pos.dtype not in (torch.float32, torch.int32) or pos.get_device() != dev or not pos.is_contiguous()
-                or tuple(pos.shape) not in ((axes, N), (1, axes, N), (B, axes, N))):
+        size, pos_dtype = pos.shape, pos.dtype
+        if (pos_dtype not in _POS_TYPES or pos.get_device() != dev or not pos.is_contiguous()
+                or size[-2:] != (axes, N) or len(size) > 3 or (len(size) == 3 and size[0] not in (1, B))):
             raise ValueError(f"pos must be a contiguous fp32 or int32 tensor [{axes}, N] or [B, {axes}, N] on the device of q")
-        pos_at, pos_type = pos.data_ptr(), LITE_FP32 if pos.dtype == torch.float32 else LITE_INT32
-        pos_a, pos_b = N, axes * N if pos.dim() == 3 and pos.shape[0] > 1 else 0
+        pos_at, pos_type = pos.data_ptr(), _POS_TYPES[pos_dtype]
+        pos_a, pos_b = N, axes * N if len(size) == 3 and size[0] > 1 else 0
     if k is not None and (q_weight is None) != (k_weight is None):
         raise ValueError("q_weight and k_weight go together")
     if k is None and (k_weight is not None or k_out is not None):
