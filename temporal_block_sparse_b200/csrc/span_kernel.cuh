@@ -262,10 +262,18 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
   }
 }
 
+// Whether some row of query tile t, which has own key tile j, does not see all its keys.
+template <int BN>
+__device__ __forceinline__ bool span_cuts(const SpanParams& p, const SpanTile& t, int j) {
+  return t.full_lo > j * BN || t.full_hi < min(j * BN + BN, p.Nk);
+}
+
 // This thread's part of a group's cleaning of own key tile j (entry q of its list): the tile goes into the item's
-// list, then its infinities and NaN become 0. The other group may use the tile at the same time: if it needs
-// it clean it cleans it too (a value is 0 then before either product that must not see it), and if its
-// rows see these values, the list, written first, brings them back.
+// list, then its infinities and NaN become 0. Both groups clean a tile that either of them needs clean, each
+// before its own product: the products then read the same values whichever group comes first (a weight that
+// underflowed to 0 makes NaN of an infinity and 0 of a cleaned one). A group that finds the tile clean
+// already finds it in the list too, which is written first; the list brings the values back to the rows
+// that see them.
 template <typename C, int BN>
 __device__ __forceinline__ void span_clean_tile(SpanCtl* ctl, uint8_t* smem, const Waiter& wt, int slot, int tid, int j, int q) {
   SpanInfo& it = ctl->info[slot];
@@ -857,6 +865,13 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
         }
         if (BIAS && idx + 1 < n_live) kp_next = key_pos(idx + 1);
         const bool masked = pre ? p.Np - j0 < BN : (mt->full_lo > j0 || mt->full_hi < j0 + BN);
+        bool unclean = false;  // some row of the item that has this tile does not see all its keys
+        if (!pre) {
+          const SpanTile& ot = it->t[grp ^ 1];  // (alternating groups: the same query tile)
+          const int j = j0 / BN, oj = j - ot.j_first;
+          unclean = span_cuts<BN>(p, *mt, j) ||
+                    (F == 1 && oj >= 0 && oj < ot.n_live - ot.n_pre && span_cuts<BN>(p, ot, j));
+        }
         wt.wait(BAR(s_full[grp]), tg & 1);
         ++tg;
         __syncwarp();
@@ -980,8 +995,8 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
             l = ml.y;
           }
         }
-        if (masked && !pre && (mt->full_lo > j0 || mt->full_hi < min(j0 + BN, p.Nk))) {
-          // Some rows do not see all keys of this tile. Their P is 0 there, but 0 times an infinity or NaN is
+        if (unclean) {
+          // Rows that do not see all keys of this tile have P = 0 there, but 0 times an infinity or NaN is
           // NaN: such values (whatever lies behind a sequence's end, say) are taken out of V before the
           // product, and rows that do see them get them back in the epilogue.
           span_clean_tile<C, BN>(ctl, smem, wt, slot, quarter * 32 + lane, j0 / BN, entry);
