@@ -492,20 +492,24 @@ __device__ __forceinline__ float2 span_tile_in_full(const SpanParams& p, uint32_
 }
 
 // Adds the non-finite values of the keys [ks, ke) that this thread's row sees (columns col0 .. col0 + NC of each
-// tile) to its row of O: those of the tiles that were cleaned for the item.
+// tile) to its row of O: those of the tiles that were cleaned for the item, as far as they are this group's
+// (alternating groups share the list, and when a group reads it the other may not be through).
 template <int D, int BN, int NC>
-__device__ __forceinline__ void span_repair(const SpanParams& p, const SpanInfo& it, uint32_t o_tmem, bool valid, int ks,
-                                         int ke, int b, int col0) {
-  // more tiles than the list holds: all tiles of the row's span
+__device__ __forceinline__ void span_repair(const SpanParams& p, const SpanInfo& it, int grp, uint32_t o_tmem, bool valid,
+                                         int ks, int ke, int b, int col0) {
+  const SpanTile& t = it.t[grp];
+  // more tiles than the list holds: all own tiles of the group
   const bool listed = it.n_bad <= kSpanBad;
-  const int x0 = listed ? 0 : ks / BN, x1 = listed ? it.n_bad : (ke + BN - 1) / BN;
+  const int n = listed ? it.n_bad : t.n_live;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     uint32_t rr[32];
     ptx::tmem_ld32(o_tmem + c * 32, rr);
     ptx::tmem_wait_ld();
-    for (int x = x0; valid && x < x1; ++x) {
-      const int j = listed ? it.bad[x] : x;
+    for (int x = 0; valid && x < n; ++x) {
+      const int entry = listed ? t.n_pre + it.bad[x] - t.j_first : t.q0 + x * t.step;
+      const int j = t.j_first + entry - t.n_pre, idx = (entry - t.q0) / t.step;
+      if (j < t.j_first || idx >= t.n_live || t.q0 + idx * t.step != entry) continue;
       const int m1 = min(ke, j * BN + col0 + NC);
       for (int m = max(ks, j * BN + col0); m < m1; ++m) {
         const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + b * p.v_stride[0] + m * p.v_stride[1] +
@@ -1015,7 +1019,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
         if (warp_valid && *static_cast<volatile const int*>(&it->n_bad) > 0) {
           int b, n, h;
           row_of(it, b, n, h);
-          span_repair<D, BN, NC>(p, *it, o_tmem, valid, ks, ke, b, col0);
+          span_repair<D, BN, NC>(p, *it, grp, o_tmem, valid, ks, ke, b, col0);
         }
       }
       // a row that saw no key: o = 0, lse = -inf (l is 0 then; a NaN score leaves its mark in l)
@@ -1030,13 +1034,17 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
         *reinterpret_cast<float2*>(ml + (src * 32 + lane) * 2) = make_float2(m_used, l);
         ptx::named_bar_sync(kAll, 256);
         float mm = -INFINITY, tot = 0.f, w[8];
+        uint32_t seen = 0u;  // the partial results that saw a key (the others' O may be anything)
 #pragma unroll
         for (int y = 0; y < 8; ++y) mm = fmaxf(mm, ml[(y * 32 + orow) * 2]);
 #pragma unroll
         for (int y = 0; y < 8; ++y) {
           const float2 e = *reinterpret_cast<const float2*>(ml + (y * 32 + orow) * 2);
           w[y] = e.y == 0.f ? 0.f : (mm == -INFINITY ? 1.f : ptx::ex2(e.x - mm));
-          if (e.y != 0.f) tot = fmaf(w[y], e.y, tot);
+          if (e.y != 0.f) {
+            tot = fmaf(w[y], e.y, tot);
+            seen |= 1u << y;
+          }
         }
         ptx::named_bar_sync(kAll, 256);
         const bool o_valid = orow < mt->rows;
@@ -1061,7 +1069,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           float4 acc4 = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int y = 0; y < 8; ++y) {
-            if (w[y] == 0.f) continue;
+            if (!(seen & (1u << y))) continue;
             const float4 e = *reinterpret_cast<const float4*>(smem + C::OFF_OST + y * C::OST_WARP + orow * 128 +
                                                               ((quad ^ (orow & 7)) << 4));
             acc4.x = fmaf(w[y], e.x, acc4.x);

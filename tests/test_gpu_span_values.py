@@ -84,3 +84,47 @@ def test_infinities_at_documents_edges_give_equal_bits_on_any_grid(d):
             bad = ~torch.isfinite(v[0, :, 0, c])
             seen[:, :, :, c] = (sees & bad).any(1)[None, :, None]
         assert torch.equal(~torch.isfinite(call()[0]), seen)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nk", [600, 9000])
+def test_infinity_far_from_a_single_token(d, Nk):
+    # The key's weight underflows in every join: of the quarters and groups of a CTA, and of the split keys. Its column
+    # is not finite all the same, whether a span ends in its tile (start 1) or not (start 0).
+    H = 3
+    q, k, v = make(Nk + d, (2, 1, H, d), (2, Nk, H, d), (2, Nk, H, d))
+    v[:, 3, :, 4] = float("inf")
+    v[:, Nk // 2, :, 9] = float("-inf")
+    spans = torch.tensor([[[0, Nk]], [[1, Nk]]], dtype=torch.int32, device="cuda")
+    slopes = torch.tensor([1.0, 0.9, 1.2], device="cuda")
+    call = lambda: la.lite_attn_span(q, k, v, spans, slopes=slopes)
+    o, lse = call()
+    assert torch.isfinite(lse).all()
+    fine = torch.ones(d, dtype=torch.bool, device="cuda")
+    fine[[4, 9]] = False
+    assert not torch.isfinite(o[..., ~fine]).any() and torch.isfinite(o[..., fine]).all()
+    same_bits(call, 30)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("Nq", [1, 40])
+def test_more_cut_tiles_with_infinities_than_an_item_lists_in_split_calls(d, Nq):
+    # Every second token of the batch sees another part of the keys, most tiles are cut and hold an infinity; parts
+    # of a split call add those of their own tiles only.
+    Nk, H = 40 * d, 2
+    q, k, v = make(Nq + d, (3, Nq, H, d), (3, Nk, H, d), (3, Nk, H, d))
+    v[:, 11 :: d, :, 3] = float("inf")
+    n = torch.arange(Nq)
+    first = (n * 131) % (Nk - 700)
+    spans = torch.stack([first, first + 13 + (n * 61) % 687], -1).int()[None].repeat(3, 1, 1)
+    spans[1, ::2, 1] = Nk
+    spans[2, :, 0] = 12  # behind the first infinity
+    spans[2, :, 1] = torch.clamp(15 + n * 5, max=Nk)
+    spans = spans.cuda()
+    call = lambda: la.lite_attn_span(q, k, v, spans)
+    o, lse = call()
+    at = torch.arange(Nk, device="cuda")
+    sees = ((at >= spans[..., :1]) & (at < spans[..., 1:]) & (at % d == 11)).any(-1)  # [B, Nq]
+    assert torch.equal(~torch.isfinite(o[..., 3]), sees[..., None].expand(-1, -1, H))
+    assert torch.isfinite(o[..., 4:]).all() and torch.isfinite(o[..., :3]).all()
+    same_bits(call, 30)
