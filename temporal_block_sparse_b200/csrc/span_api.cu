@@ -20,6 +20,7 @@ using lite_host::aligned4;
 using lite_host::DeviceContext;
 
 constexpr int kMaxDevices = 64;
+constexpr int kRopeMaxRow = 16384;  // elements of a token's row: a block holds a whole token
 
 cudaStream_t as_stream(lite_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -58,6 +59,29 @@ lite::RopeShape rope_shape(int heads, int d, int U) {
   return sh;
 }
 
+std::mutex g_rope_mu;
+
+// Sets the dynamic shared memory limit of a rope kernel on the current device, once and to the most that any
+// accepted head count takes: the limit is one value for all calls, so a call must never lower it (another
+// thread may be about to launch with more).
+template <typename T, int D, int U, int NORM, bool ONE>
+int rope_smem_limit() {
+  static bool set[kMaxDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return LITE_ERR_CUDA;
+  std::lock_guard<std::mutex> lk(g_rope_mu);
+  if (set[dev]) return LITE_OK;
+  using R = lite::RopeCfg<T, U>;
+  size_t most = 0;
+  for (int heads = 1; heads * D <= kRopeMaxRow; ++heads)
+    most = std::max(most, rope_shape(heads, D, U).bytes(R::STAGES * R::STEP, D, heads));
+  if (cudaFuncSetAttribute(lite::lite_rope_kernel<T, D, U, NORM, ONE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           int(most)) != cudaSuccess)
+    return LITE_ERR_CUDA;
+  set[dev] = true;
+  return LITE_OK;
+}
+
 template <typename T, int D, int U, int NORM, bool ONE>
 int launch_rope(lite::RopeParams p, const DeviceContext& dc, cudaStream_t stream) {
   const auto kernel = lite::lite_rope_kernel<T, D, U, NORM, ONE>;
@@ -67,9 +91,7 @@ int launch_rope(lite::RopeParams p, const DeviceContext& dc, cudaStream_t stream
   using R = lite::RopeCfg<T, U>;
   size_t smem = sq.bytes(R::STAGES * R::STEP, D, p.t[0].heads);
   if (keys) smem = std::max(smem, sk.bytes(R::STAGES * R::STEP, D, p.t[1].heads));
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) != cudaSuccess)
-    return LITE_ERR_CUDA;
+  if (smem > 48 * 1024 && rope_smem_limit<T, D, U, NORM, ONE>() != LITE_OK) return LITE_ERR_CUDA;
   const int64_t need_q = ceil_div(p.tokens, sq.tpb), need_k = keys ? ceil_div(p.tokens, sk.tpb) : 0;
   int64_t q_blocks = need_q, k_blocks = need_k;
   if (need_q + need_k > dc.sms) {
@@ -529,7 +551,7 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream) {
   if (keys && (!rope_strides_ok(a.k_stride, a.B, a.N, a.Hk, unit) || !rope_strides_ok(a.k_out_stride, a.B, a.N, a.Hk, 8)))
     return LITE_ERR_UNSUPPORTED;
   // a block holds a whole token, two units of 16 elements a thread
-  if (int64_t(a.H) * a.d > 16384 || (keys && int64_t(a.Hk) * a.d > 16384) || int64_t(a.B) * a.N > (1 << 30))
+  if (int64_t(a.H) * a.d > kRopeMaxRow || (keys && int64_t(a.Hk) * a.d > kRopeMaxRow) || int64_t(a.B) * a.N > (1 << 30))
     return LITE_ERR_UNSUPPORTED;
   DeviceContext dc;
   if (lite_host::device_context(false, &dc) != LITE_OK) return LITE_ERR_CUDA;
