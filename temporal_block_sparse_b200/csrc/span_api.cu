@@ -211,6 +211,10 @@ struct PassPlan {
   int64_t units = 0, pairs = 0, splits = 1, tiles = 0;
   int TN = 0, F = 1, alt = 0;
   int64_t items() const { return units * pairs * splits; }
+  // what an item writes where the work is split: one part of 32 rows (F = 4), or one of 128 rows a group
+  int per_item() const { return F == 4 ? 1 : 2; }
+  int rows() const { return F == 4 ? 32 : 128; }
+  int64_t part_floats(int d) const { return items() * per_item() * int64_t(lite::span_part_floats(d, rows())); }
 };
 
 struct Plan {
@@ -218,7 +222,10 @@ struct Plan {
   PassPlan pre, own;
   bool parts = false;
   double us = 0.0;       // estimated time
+  int64_t part_bytes(int d) const { return parts ? (pre.part_floats(d) + own.part_floats(d)) * int64_t(sizeof(float)) : 0; }
 };
+
+constexpr int64_t kMaxPartBytes = int64_t(1) << 30;
 
 PassPlan make_pass(int64_t units, int64_t tokens, int G, int64_t tiles) {
   PassPlan ps;
@@ -261,10 +268,8 @@ double plan_us(const Plan& pl, int d, int64_t slots) {
     us = std::max(std::max(tp, to), (double(np) * tp + double(no) * to) / double(slots) + to * 0.5);
   if (pl.parts) {
     // the join: its launch, scratch and the parts' way through L2; passes of two kinds take a launch each
-    const auto rows_of = [](const PassPlan& ps, int64_t n) { return double(n) * (ps.F == 4 ? 32.0 : 256.0); };
-    const double rows = rows_of(pl.pre, np) + rows_of(pl.own, no);
-    if (rows * (d * 4 + 8) > double(1 << 30)) return 1e30;  // no more than a gigabyte of scratch
-    us += 8.0 + rows * (d * 4 + 8) * 2.0 / 4e6 + (np && no && pl.pre.F != pl.own.F ? 4.0 : 0.0);
+    if (pl.part_bytes(d) > kMaxPartBytes) return 1e30;
+    us += 8.0 + double(pl.part_bytes(d)) * 2.0 / 4e6 + (np && no && pl.pre.F != pl.own.F ? 4.0 : 0.0);
   }
   return us;
 }
@@ -376,15 +381,16 @@ bool make_maps(const lite_span_args& a, int Np, const DeviceContext& dc, const P
   return true;
 }
 
-lite::SpanPass kernel_pass(const PassPlan& ps, int64_t slot0, int64_t slots) {
+lite::SpanPass kernel_pass(const PassPlan& ps, int64_t part0, int64_t slots) {
   lite::SpanPass k;
   k.items = int(ps.items());
   k.pairs = int(ps.pairs);
   k.splits = int(ps.splits);
   k.alt = ps.alt;
   k.TN = ps.TN;
-  k.per_item = ps.F == 4 ? 1 : 2;
-  k.slot0 = int(slot0);
+  k.per_item = ps.per_item();
+  k.rows = ps.rows();
+  k.part0 = part0;
   k.tail = int(std::min(ps.units, ceil_div(2 * slots, std::max<int64_t>(ps.pairs * ps.splits, 1))));
   return k;
 }
@@ -431,7 +437,7 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   p.v_bm = a.B > 1 && a.v_stride[0] != 0;
   p.fused = !pl.stacked;
   p.pre = kernel_pass(pl.pre, 0, slots);
-  p.own = kernel_pass(pl.own, pl.pre.items() * p.pre.per_item, slots);
+  p.own = kernel_pass(pl.own, pl.pre.part_floats(a.d), slots);
   const float scale = (a.scale > 0.f && !std::isnan(a.scale)) ? a.scale : 1.0f / std::sqrt(float(a.d));
   p.scale_log2 = scale * 1.4426950408889634f;
   if (a.cap > 0.f) {
@@ -455,9 +461,7 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   // Scratch: work counters where there are more items than CTAs (their lengths depend on the spans), and
   // the parts.
   const bool counter = items > slots;
-  const size_t floats = a.d == 64 ? lite::SpanPart<64>::FLOATS : lite::SpanPart<128>::FLOATS;
-  const size_t n_parts = pl.parts ? size_t(pl.pre.items()) * p.pre.per_item + size_t(pl.own.items()) * p.own.per_item : 0;
-  const size_t bytes = (counter ? 256 : 0) + n_parts * floats * sizeof(float);
+  const size_t bytes = (counter ? 256 : 0) + size_t(pl.part_bytes(a.d));
   Maps m;
   if (!make_maps(a, Np, dc, pl, &m)) return LITE_ERR_CUDA;
   char* ws = nullptr;

@@ -69,7 +69,8 @@ struct SpanPass {
   int alt;                  // both softmax groups take the one query tile, alternate key tiles
   int TN;                   // tokens of a query tile: 128 / G, or 32 / G (F = 4)
   int per_item;             // parts an item writes: 1 (F = 4) or 2
-  int slot0;                // index of the pass's first part
+  int rows;                 // rows of a part: 128, or 32 (F = 4)
+  long long part0;          // where the pass's parts start in scratch (floats)
   int tail;                 // last units, whose items are handed out together
 };
 
@@ -105,11 +106,8 @@ struct SpanParams {
   float cap_b[5];           // its coefficients in s^2
 };
 
-// floats of one part: O rows, then the rows' references and sums, of a 128-row tile
-template <int D>
-struct SpanPart {
-  static constexpr size_t FLOATS = 128 * D + 256;
-};
+// floats of one part: O of its rows, then the rows' references, then their sums
+__host__ __device__ constexpr size_t span_part_floats(int D, int rows) { return size_t(rows) * (D + 2); }
 
 // One query tile of an item. Its key tiles are list entries q = q0, q0 + step, .. (n_live of them): entry
 // q < n_pre is prefix tile v_first + q, the others own tile j_first + q - n_pre.
@@ -126,7 +124,7 @@ struct SpanInfo {
   int kind;              // -1 end of the work, 0 own pass, 1 prefix pass
   int alt;
   int b, hk;
-  int slot;              // index of its first part in scratch
+  int slot;              // index of its first part among the pass's
   int v_first;
   uint32_t u0;           // union index of its first tile
   int n_bad;             // own key tiles whose non-finite values were taken out of shared memory (see
@@ -193,7 +191,7 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
   it.alt = ps.alt;
   it.b = prefix ? 0 : unit / p.Hk;
   it.hk = prefix ? unit : unit - it.b * p.Hk;
-  it.slot = ps.slot0 + ((unit * ps.pairs + rank) * ps.splits + split) * ps.per_item;
+  it.slot = ((unit * ps.pairs + rank) * ps.splits + split) * ps.per_item;
   const int ntok = prefix ? p.B * p.Nq : p.Nq;
   const int tp = (prefix || p.fused) ? p.Tp : 0;
   int jlo = 0x7fffffff, jhi = 0;  // own key tiles that either query tile has to see
@@ -538,6 +536,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
   using C = SpanCfg<D, BN>;
   constexpr int NC = BN / F;  // key columns of a thread
   constexpr int PC = NC < 32 ? NC : 32;  // loaded, converted and stored at a time
+  constexpr int PR = F == 4 ? 32 : 128;  // rows of a part
   constexpr bool CAP = (MOD & kSpanCap) != 0, BIAS = (MOD & kSpanBias) != 0;
   static_assert(sizeof(SpanCtl) <= C::CTL_BYTES, "control block");
   // key positions of two tiles per warpgroup share the group's staging area
@@ -1055,7 +1054,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           n -= b * p.Nq;
         }
         const int h = it->hk * p.G + orow % p.G;
-        float* part = p.part + size_t(it->slot) * SpanPart<D>::FLOATS;
+        float* part = p.part + (it->kind == 1 ? p.pre : p.own).part0 + it->slot * span_part_floats(D, PR);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t rr[32];
@@ -1093,15 +1092,15 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
         if (it->t[0].n_live + it->t[1].n_live > 0) ptx::mbar_arrive(BAR(o_free[grp]));
         if (o_valid && quad == 0) {
           if (p.part) {
-            part[128 * D + orow] = mm;
-            part[128 * D + 128 + orow] = tot;
+            part[PR * D + orow] = mm;
+            part[PR * D + PR + orow] = tot;
           } else if (p.lse) {
             p.lse[(size_t(b) * p.H + h) * p.Nq + n] =
                 tot == 0.f ? -INFINITY : (mm + __log2f(tot)) * 0.6931471805599453f;
           }
         }
       } else if (p.part) {
-        float* part = p.part + size_t(it->slot + grp) * SpanPart<D>::FLOATS;
+        float* part = p.part + (it->kind == 1 ? p.pre : p.own).part0 + (it->slot + grp) * span_part_floats(D, PR);
         if (warp_valid) {
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -1117,8 +1116,8 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
                                      __uint_as_float(rr[4 * x + 2]), __uint_as_float(rr[4 * x + 3]));
           }
           if (valid) {
-            part[128 * D + r] = m_used;
-            part[128 * D + 128 + r] = l;
+            part[PR * D + r] = m_used;
+            part[PR * D + PR + r] = l;
           }
         }
         ptx::tc_fence_before();
@@ -1199,21 +1198,23 @@ __global__ void __launch_bounds__(256) lite_span_combine_kernel(const SpanParams
   const int b = int(bn / p.Nq), n = int(bn - static_cast<long long>(b) * p.Nq);
   const int hk = h / p.G, gh = h - hk * p.G;
   const float* part[2];
-  int count[2], at[2];
+  int count[2], at[2], rows[2];
   size_t step[2];  // from one part of the row to the next
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const SpanPass& ps = k ? p.own : p.pre;
     count[k] = 0;
+    rows[k] = ps.rows;
     if (ps.pairs == 0) continue;
     const int tok = k ? n : int(bn), tile = tok / ps.TN;
     at[k] = (tok - tile * ps.TN) * p.G + gh;
     const int pair = ps.alt ? tile : tile >> 1, unit = k ? b * p.Hk + hk : hk;
-    const size_t first = ps.slot0 + (size_t(unit) * ps.pairs + (ps.pairs - 1 - pair)) * ps.splits * ps.per_item;
-    part[k] = p.part + (first + (ps.alt ? 0 : tile & 1)) * SpanPart<D>::FLOATS;
+    const size_t first = (size_t(unit) * ps.pairs + (ps.pairs - 1 - pair)) * ps.splits * ps.per_item;
+    const size_t floats = span_part_floats(D, ps.rows);
+    part[k] = p.part + ps.part0 + (first + (ps.alt ? 0 : tile & 1)) * floats;
     // alternating groups: every part of the item holds the row
     count[k] = ps.alt ? ps.splits * ps.per_item : ps.splits;
-    step[k] = (ps.alt ? 1 : ps.per_item) * SpanPart<D>::FLOATS;
+    step[k] = (ps.alt ? 1 : ps.per_item) * floats;
   }
   const int total = count[0] + count[1];
   const auto part_at = [&](int i) -> const float* {
@@ -1229,10 +1230,10 @@ __global__ void __launch_bounds__(256) lite_span_combine_kernel(const SpanParams
     float mi = -INFINITY, li = 0.f;
     if (base + lane < total) {
       const int i = base + lane;
-      const float* q = i < count[0] ? part[0] + i * step[0] + 128 * D + at[0]
-                                    : part[1] + (i - count[0]) * step[1] + 128 * D + at[1];
+      const float* q = i < count[0] ? part[0] + i * step[0] + rows[0] * D + at[0]
+                                    : part[1] + (i - count[0]) * step[1] + rows[1] * D + at[1];
       mi = q[0];
-      li = q[128];
+      li = q[i < count[0] ? rows[0] : rows[1]];
     }
     float top = mi;
 #pragma unroll
