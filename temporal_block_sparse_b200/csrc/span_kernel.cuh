@@ -118,6 +118,9 @@ struct SpanTile {
   int j_first;
   int q0, step;
   int full_lo, full_hi;  // every row sees the own keys [full_lo, full_hi)
+  // an own tile within [quiet_lo, quiet_hi) is seen entirely by every row of the item that has it (others may be
+  // too: span_cuts tells)
+  int quiet_lo, quiet_hi;
 };
 
 struct SpanInfo {
@@ -256,7 +259,22 @@ __device__ __forceinline__ void span_decode(const SpanParams& p, int idx, int la
     t.n_live = t.n_pre + (t.rows ? max(0, j1 - j0) : 0);
     t.q0 = ps.alt ? g : 0;
     t.step = ps.alt ? 2 : 1;
-    if (ps.alt) t.n_live = (t.n_live + 1 - g) >> 1;
+    t.quiet_lo = t.full_lo;
+    t.quiet_hi = t.full_hi;
+  }
+  if (ps.alt) {
+    it.t[1].n_live >>= 1;
+    it.t[0].n_live -= it.t[1].n_live;
+    return;
+  }
+  // where the other query tile has own key tiles that are cut for its rows: those before and behind its full range
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const SpanTile& o = it.t[g ^ 1];
+    const int first = o.j_first * BN, end = min((o.j_first + o.n_live - o.n_pre) * BN, p.Nk);
+    if (first >= end) continue;
+    if (first < o.full_lo) it.t[g].quiet_lo = max(it.t[g].full_lo, o.full_lo);
+    if (o.full_hi < end) it.t[g].quiet_hi = min(it.t[g].full_hi, o.full_hi);
   }
 }
 
@@ -498,16 +516,16 @@ __device__ __forceinline__ void span_repair(const SpanParams& p, const SpanInfo&
   const SpanTile& t = it.t[grp];
   // more tiles than the list holds: all own tiles of the group
   const bool listed = it.n_bad <= kSpanBad;
-  const int n = listed ? it.n_bad : t.n_live;
+  const int end = t.j_first + (it.alt ? it.t[0].n_live + it.t[1].n_live : t.n_live) - t.n_pre;
+  const int n = listed ? it.n_bad : end - t.j_first;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     uint32_t rr[32];
     ptx::tmem_ld32(o_tmem + c * 32, rr);
     ptx::tmem_wait_ld();
     for (int x = 0; valid && x < n; ++x) {
-      const int entry = listed ? t.n_pre + it.bad[x] - t.j_first : t.q0 + x * t.step;
-      const int j = t.j_first + entry - t.n_pre, idx = (entry - t.q0) / t.step;
-      if (j < t.j_first || idx >= t.n_live || t.q0 + idx * t.step != entry) continue;
+      const int j = listed ? it.bad[x] : t.j_first + x;
+      if (j < t.j_first || j >= end || (it.alt && ((t.n_pre + j - t.j_first) & 1) != grp)) continue;
       const int m1 = min(ke, j * BN + col0 + NC);
       for (int m = max(ks, j * BN + col0); m < m1; ++m) {
         const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + b * p.v_stride[0] + m * p.v_stride[1] +
@@ -867,11 +885,14 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           ptx::named_bar_sync(gbar, 128);
         }
         if (BIAS && idx + 1 < n_live) kp_next = key_pos(idx + 1);
-        const bool masked = pre ? p.Np - j0 < BN : (mt->full_lo > j0 || mt->full_hi < j0 + BN);
-        bool unclean = false;  // some row of the item that has this tile does not see all its keys
-        if (!pre) {
+        bool masked = false;   // some row of the query tile does not see all keys of this tile
+        bool unclean = false;  // some row of the item that has this tile does not see all keys that it holds
+        if (pre) {
+          masked = p.Np - j0 < BN;
+        } else if (j0 < mt->quiet_lo || j0 + BN > mt->quiet_hi) {
           const SpanTile& ot = it->t[grp ^ 1];  // (alternating groups: the same query tile)
           const int j = j0 / BN, oj = j - ot.j_first;
+          masked = mt->full_lo > j0 || mt->full_hi < j0 + BN;
           unclean = span_cuts<BN>(p, *mt, j) ||
                     (F == 1 && oj >= 0 && oj < ot.n_live - ot.n_pre && span_cuts<BN>(p, ot, j));
         }
