@@ -60,6 +60,11 @@ __device__ __forceinline__ float abs_max3(float a, float b, float c) {
 
 constexpr int kSpanCap = 1, kSpanBias = 2;  // MOD bits of the kernel
 
+// Biases up to this (log2 units) are kept out of the scores exactly. A row's reference is a 32-bit number of the
+// bias's size, so it meets the row's maximum within a few units in its last place: 8 here, far from the
+// ends of 2^x. Beyond, a score and its bias are one 32-bit sum.
+constexpr float kSpanFarBias = 67108864.f;  // 2^26
+
 // One pass over query tiles: the prefix pass (tokens of the whole batch against the shared prefix) or
 // the own pass (tokens of one batch entry against its keys).
 struct SpanPass {
@@ -422,6 +427,10 @@ __device__ __forceinline__ void span_rescale(uint32_t o_tmem, float alpha) {
 // A key tile for which the short way does not do (a span ends in it, scores near the cap, rows on both sides of it,
 // given positions): every score of the warp's rows in full, back into TMEM, then the exponentials. Keys
 // [lo, hi) of this thread's NC columns are seen. Takes and returns (reference, row sum).
+//
+// Far from its keys a row's bias is much larger than what its scores differ by: at 2^19 log2 units a 32-bit sum of both
+// is good to 2^-5. So the least bias among the keys seen (`off`) stays out of the sums: a score is s + (off - bias),
+// off - bias one rounding of a small number, and off is taken into account with the reference.
 template <int D, int NC, int MOD, int F>
 __device__ __forceinline__ float2 span_tile_in_full(const SpanParams& p, uint32_t s_tmem, uint32_t o_tmem, int quarter,
                                                  int lo, int hi, float base, float slope, float qp, const float* kpos,
@@ -429,18 +438,59 @@ __device__ __forceinline__ float2 span_tile_in_full(const SpanParams& p, uint32_
   constexpr bool CAP = (MOD & kSpanCap) != 0, BIAS = (MOD & kSpanBias) != 0;
   constexpr int PC = NC < 32 ? NC : 32;
   const int col0 = F == 1 ? 0 : quarter * NC;
+  // the keys seen among columns PC * c .. as bits: one select per column
+  const auto seen = [&](int c) -> uint32_t {
+    const int a = min(max(lo - PC * c, 0), 32), z = min(max(hi - PC * c, 0), 32);
+    const uint32_t upto = z >= 32 ? 0xffffffffu : ((1u << z) - 1u);
+    const uint32_t below = a >= 32 ? 0xffffffffu : ((1u << a) - 1u);
+    return upto & ~below;
+  };
+  // column x is lowered by the bias and raised by off: step * |from + x| + rest
+  float off = 0.f, step = -slope, from = base, rest = 0.f;
+  if constexpr (BIAS) {
+    if (kpos) {
+      float near = INFINITY, far = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < NC / PC; ++c) {
+        const uint32_t bits = seen(c);
+#pragma unroll
+        for (int x = 0; x < PC; ++x) {
+          const float dist = fabsf(kpos[PC * c + x] - qp);
+          near = fminf(near, (bits & (1u << x)) ? dist : INFINITY);
+          far = fmaxf(far, (bits & (1u << x)) ? dist : 0.f);
+        }
+      }
+      off = fminf(slope * near, slope * far);
+      if (!(fabsf(off) <= kSpanFarBias)) off = 0.f;
+      rest = off;
+    } else {
+      const float a = float(max(lo, 0)), z = float(min(hi, NC) - 1);
+      // the least bias is at the first or last of them, or (rows amid the columns) at the row's own position
+      const bool one_side = base >= 0.f || base <= 1.f - NC;
+      const float end = (base < 0.f) == (slope >= 0.f) ? z : a;
+      off = slope * fabsf(base + end);
+      if (!one_side)
+        off = fminf(fminf(slope * fabsf(base + a), slope * fabsf(base + z)), slope * fabsf(base + fminf(fmaxf(-base, a), z)));
+      if (!(fabsf(off) <= kSpanFarBias)) off = 0.f;
+      rest = off;
+      if (one_side) {
+        // the bias grows by |slope| a column from that end, where it is off but for the rounding of off (and of
+        // the distance, where that takes more than 24 bits: dist + lost is the sum itself)
+        const float dist = base + end, lost = end - (dist - base);
+        step = -fabsf(slope);
+        from = -end;
+        rest = fmaf(dist < 0.f ? slope : -slope, lost, fmaf(-slope, fabsf(dist), off));
+      }
+    }
+  }
   float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
   float v[PC];
 #pragma unroll 1
   for (int c = 0; c < NC / PC; ++c) {
     span_load<PC>(s_tmem + col0 + c * PC, v);
     ptx::tmem_wait_ld();
-    // the keys seen among these columns as bits: one select per column
-    const int a = min(max(lo - PC * c, 0), 32), z = min(max(hi - PC * c, 0), 32);
-    const uint32_t upto = z >= 32 ? 0xffffffffu : ((1u << z) - 1u);
-    const uint32_t below = a >= 32 ? 0xffffffffu : ((1u << a) - 1u);
-    const uint32_t bits = upto & ~below;
-    const float at = base + float(PC * c);
+    const uint32_t bits = seen(c);
+    const float at = from + float(PC * c);
     const float* kc = kpos + PC * c;
     if constexpr (CAP) {
       float big = 0.f;
@@ -473,7 +523,7 @@ __device__ __forceinline__ float2 span_tile_in_full(const SpanParams& p, uint32_
     }
 #pragma unroll
     for (int x = 0; x < PC; ++x) {
-      if (BIAS) v[x] = fmaf(-slope, fabsf(kpos ? kc[x] - qp : at + float(x)), v[x]);
+      if (BIAS) v[x] += fmaf(step, fabsf(kpos ? kc[x] - qp : at + float(x)), rest);
       v[x] = (bits & (1u << x)) ? v[x] : -INFINITY;
     }
     span_max<PC>(v, m);
@@ -483,7 +533,7 @@ __device__ __forceinline__ float2 span_tile_in_full(const SpanParams& p, uint32_
       ptx::tmem_st16(s_tmem + col0, reinterpret_cast<uint32_t(&)[16]>(v));
   }
   ptx::tmem_wait_st();
-  const float loc = span_max4(m);
+  const float loc = span_max4(m) - off;
   float m_used = ml.x, l = ml.y, alpha = 1.f;
   const bool need = loc > m_used + kRescaleLog2;
   if (need) {
@@ -491,7 +541,7 @@ __device__ __forceinline__ float2 span_tile_in_full(const SpanParams& p, uint32_
     m_used = loc;
     l *= alpha;
   }
-  const float neg_m = m_used == -INFINITY ? 0.f : -m_used;
+  const float neg_m = m_used == -INFINITY ? 0.f : -off - m_used;
   const float2 nm2 = make_float2(neg_m, neg_m);
   float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
@@ -859,6 +909,11 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           qp = p.q_pos ? __ldg(p.q_pos + b * p.q_pos_b + n) : float(p.Np + p.Nk - p.Nq + n);
         }
       }
+      // no row of the warp has a slope too steep, or keys too far away, for the short way below
+      bool gentle = true;
+      if (BIAS)
+        gentle = __all_sync(0xffffffffu, !valid || (fabsf(slope) * PC <= (CAP ? 30.f : 60.f) &&
+                                                     fabsf(slope) * (fabsf(qp) + float(p.Np + p.Nk)) <= kSpanFarBias));
       float m_used = -INFINITY;  // exponent reference (lazy rescale), log2 units
       float l = 0.f;             // row sum relative to m_used
       // given position of key r of the group's tile idx
@@ -907,8 +962,7 @@ __global__ void __launch_bounds__(320, AttnCfg<D, BN>::CTAS_PER_SM)
           const float sg = base < 0.f ? slope : -slope;
           bool fast = !masked && !given;
           if (BIAS)
-            fast = fast && __all_sync(0xffffffffu, !valid || ((base >= 0.f || base <= 1.f - NC) &&
-                                                               fabsf(slope) * PC <= (CAP ? 30.f : 60.f)));
+            fast = fast && gentle && __all_sync(0xffffffffu, !valid || base >= 0.f || base <= 1.f - NC);
           float loc = -INFINITY;  // the tile's row maximum, or a reference near it (log2 units)
           float v[MOD == 0 ? NC / PC : 2][PC];
           if (fast) {
