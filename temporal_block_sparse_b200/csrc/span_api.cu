@@ -209,7 +209,9 @@ int check_attention(const lite_span_args& a, bool prefix) {
 // `tokens` tokens against `tiles` key tiles.
 struct PassPlan {
   int64_t units = 0, pairs = 0, splits = 1, tiles = 0;
-  int TN = 0, F = 1, alt = 0;
+  int TN = 0, F = 1;
+  bool one = false;  // one query tile only
+  int alt = 0;       // and both softmax groups take it: with F = 4 (which joins them in the CTA), or where there are parts
   int64_t items() const { return units * pairs * splits; }
   // what an item writes where the work is split: one part of 32 rows (F = 4), or one of 128 rows a group
   int per_item() const { return F == 4 ? 1 : 2; }
@@ -222,6 +224,11 @@ struct Plan {
   PassPlan pre, own;
   bool parts = false;
   double us = 0.0;       // estimated time
+  void set_parts() {
+    parts = true;
+    pre.alt = pre.one;
+    own.alt = own.one;
+  }
   int64_t part_bytes(int d) const { return parts ? (pre.part_floats(d) + own.part_floats(d)) * int64_t(sizeof(float)) : 0; }
 };
 
@@ -235,8 +242,9 @@ PassPlan make_pass(int64_t units, int64_t tokens, int G, int64_t tiles) {
   ps.F = tokens * G <= 32 ? 4 : 1;
   ps.TN = (ps.F == 4 ? 32 : 128) / G;
   const int64_t tq = ceil_div(tokens, ps.TN);
-  ps.alt = tq == 1;
-  ps.pairs = ceil_div(tq, ps.alt ? 1 : 2);
+  ps.one = tq == 1;
+  ps.alt = ps.one && ps.F == 4;
+  ps.pairs = ceil_div(tq, 2);
   return ps;
 }
 
@@ -249,6 +257,8 @@ double item_us(const PassPlan& ps, int d, double t, bool busy) {
     tile = d == 64 ? (busy ? 1.0 : 0.75) : (busy ? 1.35 : 1.05);
   else if (ps.alt)
     tile = d == 64 ? (busy ? 0.9 : 0.7) : (busy ? 1.4 : 1.1);
+  else if (ps.one)  // unsplit, one group takes all tiles (64 rows, 144 heads, 256 tiles, d = 128: 484 us, 396 split in two)
+    tile = d == 64 ? (busy ? 1.25 : 1.2) : 1.85;
   else
     tile = d == 64 ? (busy ? 1.75 : 1.25) : (busy ? 2.4 : 2.1);
   return 4.0 + tile * t;
@@ -286,7 +296,7 @@ void choose_splits(Plan& pl, int d, int64_t slots) {
     const int64_t t = ceil_div(longest, s);
     c.pre.splits = std::max<int64_t>(1, ceil_div(c.pre.tiles, t));
     c.own.splits = std::max<int64_t>(1, ceil_div(c.own.tiles, t));
-    c.parts = true;
+    c.set_parts();
     if (c.pre.items() + c.own.items() > most) break;
     c.us = plan_us(c, d, slots);
     if (c.us < pl.us) pl = c;
@@ -302,14 +312,13 @@ Plan make_plan(const lite_span_args& a, int Np, int Tp, int Tk, int64_t slots) {
   const bool flat = a.B > 1 && a.q_stride[0] > 0 && (a.Nq == 1 || a.q_stride[0] == int64_t(a.Nq) * a.q_stride[1]);
   if (Np > 0 && flat) {
     Plan c;
-    c.stacked = c.parts = true;
+    c.stacked = true;
     c.pre = make_pass(a.Hk, int64_t(a.B) * a.Nq, G, Tp);
     if (a.Nk > 0) c.own = make_pass(int64_t(a.B) * a.Hk, a.Nq, G, Tk);
+    c.set_parts();
     choose_splits(c, a.d, slots);
     if (c.us < best.us) best = c;
   }
-  // One tile and no join: both groups on it would need one (F = 4 joins them in the CTA).
-  if (!best.parts && best.own.F == 1) best.own.alt = 0;
   return best;
 }
 
