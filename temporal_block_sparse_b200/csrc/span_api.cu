@@ -503,8 +503,8 @@ int run_span(const lite_span_args& a, bool prefix, cudaStream_t stream) {
   if (!st && pl.parts) {
     const int64_t threads = int64_t(a.B) * a.Nq * a.H * (a.d / 4);
     const unsigned blocks = unsigned(ceil_div(threads, 256));
-    // Launched while the parts are still being written (it waits for them itself), so that its
-    // start-up is hidden.
+    // The join may start once the last CTA of the kernel before has ended, and waits itself until that kernel's
+    // writes can be read: without the gap between dependent launches, 2 us less (20.5 against 22.5 us for a tiny call).
     cudaLaunchConfig_t cfg;
     std::memset(&cfg, 0, sizeof(cfg));
     cfg.gridDim = dim3(blocks);

@@ -1295,7 +1295,7 @@ __global__ void __launch_bounds__(256) lite_span_combine_kernel(const SpanParams
   const auto part_at = [&](int i) -> const float* {
     return i < count[0] ? part[0] + i * step[0] + at[0] * D : part[1] + (i - count[0]) * step[1] + at[1] * D;
   };
-  // the scratch is the kernel's before this one in the stream
+  // the scratch is written by the kernel before this one in the stream, which has ended but whose writes may not be seen yet
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float m = -INFINITY, tot = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
