@@ -89,15 +89,12 @@ int device_cache(DeviceCache** out) {
   return LITE_OK;
 }
 
-// The library-owned stream-ordered pool of a device, created on first use by a pooled call.
-int ensure_pool(DeviceCache* c) {
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (c->pool) return LITE_OK;
+int create_pool(int dev, cudaMemPool_t* out) {
   cudaMemPoolProps props;
   std::memset(&props, 0, sizeof(props));
   props.allocType = cudaMemAllocationTypePinned;
   props.location.type = cudaMemLocationTypeDevice;
-  props.location.id = c->dev;
+  props.location.id = dev;
   cudaMemPool_t pool = nullptr;
   if (cudaMemPoolCreate(&pool, &props) != cudaSuccess) return LITE_ERR_CUDA;
   uint64_t keep = ~uint64_t(0);
@@ -105,8 +102,21 @@ int ensure_pool(DeviceCache* c) {
     cudaMemPoolDestroy(pool);
     return LITE_ERR_CUDA;
   }
-  c->pool = pool;
+  *out = pool;
   return LITE_OK;
+}
+
+// The library-owned stream-ordered pool of a device, created on first use by a pooled call. That call may be
+// inside a stream capture, which refuses to create a pool (and ends) unless this thread's capture mode is relaxed
+// meanwhile: nothing here goes to a stream.
+int ensure_pool(DeviceCache* c) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (c->pool) return LITE_OK;
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return LITE_ERR_CUDA;
+  const int st = create_pool(c->dev, &c->pool);
+  if (cudaThreadExchangeStreamCaptureMode(&mode) != cudaSuccess) return LITE_ERR_CUDA;
+  return st;
 }
 
 }  // namespace
