@@ -442,12 +442,12 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream);
  *                  are not looked at. 16-byte aligned.
  *  o          out  device bf16 [B, Nq, H, d], contiguous. lse out device fp32 [B, H, Nq], or NULL.
  *  spans      in   device int32 [span_batches, Nq, 2], 8-byte aligned, or NULL: all keys.
- *                  span_batches 1 (one table for all entries) or B.
+ *                  span_batches 1 (one table for all entries) or B; others are refused.
  *  scale           <= 0 or NaN selects 1/sqrt(d). cap: 0 = none; negative, infinite or NaN is refused.
  *  slopes     in   device fp32 [H], or NULL. With slopes:
  *  q_pos, k_pos    device fp32 [pos_batches, Nq] and [pos_batches, Nk], or NULL each: the queries are
  *                  the last Nq of all positions (Np + Nk - Nq + n), key m is at Np + m, prefix
- *                  key m at m (prefix_pos, fp32 [Np], replaces it). pos_batches 1 or B.
+ *                  key m at m (prefix_pos, fp32 [Np], replaces it). pos_batches 1 or B; others are refused.
  *  d in {64, 128}; Hk divides H, H / Hk <= 128; B * Nq, Nk, Np, B * H <= 2^30, with slopes Nk + Np and
  *  Nq <= 2^24. Nk = 0 is refused here (lite_attn_prefix allows it).
  *

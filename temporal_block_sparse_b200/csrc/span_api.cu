@@ -185,6 +185,9 @@ int check_attention(const lite_span_args& a, bool prefix) {
   if (a.H % a.Hk) return LITE_ERR_INVALID_ARG;
   if (std::isnan(a.cap) || a.cap < 0.f || std::isinf(a.cap)) return LITE_ERR_INVALID_ARG;
   if (!a.slopes && (a.q_pos || a.k_pos || a.prefix_pos)) return LITE_ERR_INVALID_ARG;
+  // a table for some of the batch entries would be read past its end
+  if (a.spans && a.span_batches != 1 && a.span_batches != a.B) return LITE_ERR_INVALID_ARG;
+  if ((a.q_pos || a.k_pos) && a.pos_batches != 1 && a.pos_batches != a.B) return LITE_ERR_INVALID_ARG;
   const int t = tile_for(a.d);
   if (!t || a.H / a.Hk > 128) return LITE_ERR_UNSUPPORTED;
   if (!aligned16(a.q) || !aligned16(a.o) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.k_prefix) ||
