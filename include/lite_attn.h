@@ -387,8 +387,9 @@ int lite_dropped_mass(const float* lse_live, const float* lse_full, float* row_m
  *  q_out, k_out   out  device bf16, same shapes. Either may be its input itself (same type and
  *                      strides); other overlaps are not allowed.
  *  *_stride            strides in elements of the batch, token and head dimension (the head dim is
- *                      contiguous): non-negative, multiples of 16 bytes. Strides of dimensions with one
- *                      entry are not looked at. An output's rows may not overlap.
+ *                      contiguous): multiples of 16 bytes, an input's non-negative, an output's positive.
+ *                      Strides of dimensions with one entry are not looked at. An output's rows may not
+ *                      overlap.
  *  q_weight, k_weight  device fp32, 16-byte aligned; NULL without norm.
  *  pairing        0: pair p = elements (2p, 2p + 1); 1: (p, p + d/2).
  *  freq, axis     HOST [d/2]: angular frequency and axis of each pair (freq 0 leaves a pair as it is).

@@ -28,12 +28,12 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // ------------------------------------------------------------------------------------- rotation
 
-// Strides (batch, token, head) of a [B, N, heads, d] tensor: non-negative, multiples of `unit`
+// Strides (batch, token, head) of a [B, N, heads, d] tensor: at least `least`, multiples of `unit`
 // elements (16 bytes) wherever the dimension has more than one entry.
-bool rope_strides_ok(const int64_t* s, int B, int N, int heads, int unit) {
+bool rope_strides_ok(const int64_t* s, int B, int N, int heads, int unit, int least) {
   const int n[3] = {B, N, heads};
   for (int x = 0; x < 3; ++x)
-    if (n[x] > 1 && (s[x] < 0 || s[x] % unit)) return false;
+    if (n[x] > 1 && (s[x] < least || s[x] % unit)) return false;
   return true;
 }
 
@@ -562,9 +562,11 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream) {
   if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.q_out) || !aligned16(a.k_out) || !aligned16(a.q_weight) ||
       !aligned16(a.k_weight) || !aligned4(a.pos))
     return LITE_ERR_UNSUPPORTED;
-  if (!rope_strides_ok(a.q_stride, a.B, a.N, a.H, unit) || !rope_strides_ok(a.q_out_stride, a.B, a.N, a.H, 8))
+  // (an output stride of 0 would have several rows written to one place)
+  if (!rope_strides_ok(a.q_stride, a.B, a.N, a.H, unit, 0) || !rope_strides_ok(a.q_out_stride, a.B, a.N, a.H, 8, 8))
     return LITE_ERR_UNSUPPORTED;
-  if (keys && (!rope_strides_ok(a.k_stride, a.B, a.N, a.Hk, unit) || !rope_strides_ok(a.k_out_stride, a.B, a.N, a.Hk, 8)))
+  if (keys && (!rope_strides_ok(a.k_stride, a.B, a.N, a.Hk, unit, 0) ||
+               !rope_strides_ok(a.k_out_stride, a.B, a.N, a.Hk, 8, 8)))
     return LITE_ERR_UNSUPPORTED;
   // a block holds a whole token, two units of 16 elements a thread
   if (int64_t(a.H) * a.d > kRopeMaxRow || (keys && int64_t(a.Hk) * a.d > kRopeMaxRow) || int64_t(a.B) * a.N > (1 << 30))
