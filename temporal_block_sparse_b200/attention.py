@@ -225,12 +225,13 @@ class ChunkedAttention:
         n = N // ft
         if self._done + n > self.frames:
             raise ValueError(f"the cache holds {self.frames} frames: {self._done} are taken")
-        if self._k is None:
-            shape = (B, self.frames * ft, Hk, d)
+        shape = (B, self.frames * ft, Hk, d)
+        if self._done and shape != tuple(self._k.shape):
+            raise ValueError("batch size, key heads and head dimension must stay as in the first chunk")
+        if self._k is None or not self._done and (shape != tuple(self._k.shape) or q.device != self._k.device):
+            # (a first chunk that was refused further down decides nothing)
             self._k = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
             self._v = torch.empty_like(self._k)
-        if (B, Hk, d) != (self._k.shape[0], self._k.shape[2], self._k.shape[3]):
-            raise ValueError("batch size, key heads and head dimension must stay as in the first chunk")
         at, end = self._done * ft, (self._done + n) * ft
         if start is None:
             start = at + (0 if self._hk is None else self._hk.shape[0])
