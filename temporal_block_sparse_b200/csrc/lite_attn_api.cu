@@ -65,7 +65,10 @@ cudaStream_t as_stream(lite_stream_t s) { return reinterpret_cast<cudaStream_t>(
 // Per-device set-up that every entry point needs: SM count, the status word's device address and
 // the tensor-map encoder. It allocates nothing; the scratch pool is created separately, on the first
 // pooled call (ensure_pool).
+// It also forgets the error of an earlier call of this thread (one without room for its scratch, say), which
+// that call returned: the checks after this call's launches would find it again.
 int device_cache(DeviceCache** out) {
+  (void)cudaGetLastError();
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return LITE_ERR_CUDA;
   std::lock_guard<std::mutex> lk(g_mu);
