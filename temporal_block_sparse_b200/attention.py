@@ -182,7 +182,10 @@ class ChunkedAttention:
         and those before it), or the last `window` frames only. (The history is always seen.)
     cap, slopes: as in lite_attn_span; distances count tokens of history and cache.
 
-    The cache holds `frames` frames; reset() empties it for the next video.
+    The cache holds `frames` frames; reset() empties it for the next video. Every call takes its frames for good: the
+    next one comes after them (several passes over one chunk are not offered). A chunk of one frame without a
+    window can be captured into a graph, which then repeats that chunk at its place in the cache; others make
+    their span table on the host in each call and cannot.
     """
 
     def __init__(self, rope: AxisRope, frames: int, frame_tokens: int, window: Optional[int] = None, cap: float = 0.0,
