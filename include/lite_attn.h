@@ -214,8 +214,8 @@ int lite_set_kernel_events(void* before, void* after);
  * lite_scratch_pool_bytes -- measurement hook. *reserved = device memory, in bytes, that the
  * library's scratch pool on the current device holds (its stream-ordered pool keeps freed memory
  * for reuse); 0 while no pooled call has run on the device, since the pool is created by the
- * first lite_attn_fwd / lite_attn_fwd_ex call. Makes no allocation. LITE_ERR_INVALID_ARG for a
- * NULL pointer.
+ * first lite_attn_fwd / lite_attn_fwd_ex / lite_attn_fwd_list call, or lite_attn_span / lite_attn_prefix
+ * call that splits its work. Makes no allocation. LITE_ERR_INVALID_ARG for a NULL pointer.
  */
 int lite_scratch_pool_bytes(long long* reserved);
 
@@ -233,8 +233,8 @@ int lite_scratch_pool_bytes(long long* reserved);
  * array of LITE_NOALLOC_SCRATCH_BYTES (8 MiB) that the library defines in device memory. Every GPU
  * that loads the library holds that array until the process exits. This call makes no cudaMalloc,
  * cudaFree or other allocating call, and creates no memory pool (the scratch pool behind
- * lite_attn_fwd is created by the first lite_attn_fwd / lite_attn_fwd_ex call on a device, never
- * by this one; lite_scratch_pool_bytes reports whether it exists).
+ * lite_attn_fwd is created by the first pooled call on a device, never by this one;
+ * lite_scratch_pool_bytes reports whether it exists).
  *
  *  - Limit: the layer's scratch must fit in 8 MiB. With R = B*H*T and T = ceil(N / tile) it is
  *    up256(2*R*T) + 2*up256(4*R) + 512 bytes (up256 rounds up to a multiple of 256), about
@@ -435,7 +435,8 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream);
  *   lse = ln sum exp(s).
  * Query head h uses key head h / (H / Hk). Key tiles that no row of a query tile sees are not loaded.
  * Keys outside a row's span do not reach its result, whatever k and v hold there (NaN and infinities
- * included); a value of v that is not finite makes its column of the rows that see it not finite.
+ * included); a value of v that is not finite makes its column of the rows that see it not finite (an
+ * infinity may come out as NaN there, where its weight is 0 in 32 bits).
  *
  *  q          in   device bf16 [B, Nq, H, d]; k, v in device bf16 [B, Nk, Hk, d]; strides in elements
  *                  (batch, token, head; the head dim is contiguous), positive multiples of 8. A batch
@@ -449,6 +450,11 @@ int lite_qk_rope(const lite_rope_args* args, lite_stream_t stream);
  *  q_pos, k_pos    device fp32 [pos_batches, Nq] and [pos_batches, Nk], or NULL each: the queries are
  *                  the last Nq of all positions (Np + Nk - Nq + n), key m is at Np + m, prefix
  *                  key m at m (prefix_pos, fp32 [Np], replaces it). pos_batches 1 or B; others are refused.
+ *                  (In a padded batch the default positions are those of the padded end: q_pos gives a
+ *                  sequence's own. Where all its queries come after its keys, only lse differs.)
+ *                  Distances are 32-bit differences, exact for whole positions up to 2^24. A bias of up to
+ *                  4e7 is kept out of the 32-bit scores, so that weights are as exact far from the keys
+ *                  as near them; beyond, score and bias are one 32-bit sum.
  *  d in {64, 128}; Hk divides H, H / Hk <= 128; B * Nq, Nk, Np, B * H <= 2^30, with slopes Nk + Np and
  *  Nq <= 2^24. Nk = 0 is refused here (lite_attn_prefix allows it).
  *

@@ -19,7 +19,7 @@
 // columns. Where there is one query tile only, both softmax groups take it, on alternate key
 // tiles (`alt`), and this tile's QK^T is issued before the product of the other group's tile. With F = 4
 // the eight partial results of a row are joined in the CTA. One token of 8 sequences of up to 32760
-// keys (40 heads over 8, d = 128, 839 MB): 249 us with one group and one warp at work, 169 us so.
+// keys (40 heads over 8, d = 128, 839 MB): 249 us with one group and one warp at work, 161-170 us so.
 //
 // Work items. An item is a pair of query tiles (one per softmax warpgroup), or one tile (alt), and a
 // part of the key tiles they see: [prefix tiles][own tiles lo .. hi), of which split s of S takes its
@@ -33,9 +33,10 @@
 // A key tile that every row of the query tile sees entirely takes no mask instruction.
 //
 // What bounds it. Long rows: the S -> P -> PV -> QK chain of each query tile, as in lite_attn_kernel
-// (frame-causal 480p layer, 40 heads, d = 128: 11.5 ms, 1000 TFLOP/s; tensor pipe 47% busy, exponential
-// unit 47%, issue slots 33%). d = 64: the exponential unit and issue slots. Few rows: HBM (839 MB in
-// 150 us, 5.6 TB/s). Small calls: launches.
+// (frame-causal 480p layer, 40 heads, d = 128: 11.3-11.6 ms, 1000 TFLOP/s; tensor pipe 47% busy, exponential
+// unit 48%, issue slots 34%). d = 64: issue slots (55%) before the exponential unit (38%). Few rows: HBM (839 MB
+// in 154 us, 5.5 TB/s, and the join). Small calls: the chain of key tiles of an item, and the host's call
+// (60 items of ten key tiles each, d = 64: 16 us on the GPU, 18 us of the host).
 //
 // Every wait is bounded as in lite_attn_kernel; on expiry the status word is set and the CTA drains.
 #pragma once
